@@ -32,6 +32,7 @@ FP8Q_ERR_ALIGN = 3
 FP8Q_ERR_CUDA = 4
 FP8Q_ERR_TIMEOUT = 5
 FP8Q_ERR_UNSUPPORTED = 6
+FP8Q_ERR_OFFSETS = 7
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int64
@@ -66,6 +67,19 @@ _SIGS = {
     "fp8q_linear_dgrad": ([_P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _P], ctypes.c_int),
     "fp8q_linear_wgrad": ([_P, _P, _P, _P, _I, _I, _I, _P, _I, _P], ctypes.c_int),
     "fp8q_linear_wgrad_acc_f32": ([_P, _P, _P, _P, _I, _I, _I, _P, _I, _P], ctypes.c_int),
+    "fp8q_add_rmsnorm_quant": ([_P, _P, _P, _I, _I, _I, _I, _F, _P, _I, _P, _P, _I, _P],
+                               ctypes.c_int),
+    "fp8q_grouped_padded_rows": ([_I, _I], ctypes.c_int64),
+    "fp8q_grouped_linear_fwd": ([_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P],
+                                ctypes.c_int),
+    "fp8q_grouped_linear_dgrad": ([_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P],
+                                  ctypes.c_int),
+    "fp8q_grouped_linear_wgrad": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P],
+                                  ctypes.c_int),
+    "fp8q_grouped_transpose_quant_bf16": ([_P, _P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _I, _P],
+                                          ctypes.c_int),
+    "fp8q_grouped_transpose_quant_fp8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _P],
+                                         ctypes.c_int),
     "fp8q_debug_wait_timeout": ([_I, _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -534,6 +548,243 @@ def linear_wgrad_acc_f32(qdyT, sdy_c, qxT, sx_c, dw, stream=None):
     _check(_lib.fp8q_linear_wgrad_acc_f32(_ptr(qdyT), _ptr(sdy_c), _ptr(qxT), _ptr(sx_c), M, N,
                                           K, _ptr(dw), _rows_dense(dw, "dw"), _stream(stream)),
            "fp8q_linear_wgrad_acc_f32")
+
+
+# --------------------------------------------------------------------------
+# One weight per expert (ragged row groups), and the norm in front of it
+# --------------------------------------------------------------------------
+
+def _row_stride(t, name):
+    """Row stride of a matrix with dense rows (a single row has none: its length)."""
+    if t.stride(-1) != 1 and t.shape[1] > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
+
+
+def _run(fn, where, stream, ref, *args):
+    """Call `fn` on the device of `ref` (the current one or not), on `stream` or that
+    device's current stream."""
+    if ref.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(ref.device):
+            _check(fn(*args, _stream(stream)), where)
+
+
+def _together(*named):
+    """Every operand lies on the first one's device."""
+    dev = named[0][0].device
+    for t, n in named[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError("%s must be on %s, got %s" % (n, dev, t.device))
+
+
+def _offsets(offsets, experts=None):
+    """int32 [E + 1]; returns E."""
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a torch.Tensor")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or (
+            experts is not None and offsets.numel() != experts + 1):
+        raise ValueError("offsets must be an int32 tensor [%s], got %s %s" % (
+            "E + 1" if experts is None else experts + 1, tuple(offsets.shape), offsets.dtype))
+    _dense(offsets, "offsets")
+    return offsets.numel() - 1
+
+
+def grouped_padded_rows(M, E) -> int:
+    """Columns P of the transposed arrays of a grouped call over M rows and E experts that
+    are enough whatever the offsets are (a multiple of 128)."""
+    n = int(_lib.fp8q_grouped_padded_rows(int(M), int(E)))
+    if n < 0:
+        raise ValueError("grouped_padded_rows: M=%d E=%d" % (M, E))
+    return n
+
+
+def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
+    """a3 behind a residual addition: h = bf16(x + res) [M,H] (may be x or res itself), then
+    RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]. Its backward is
+    rmsnorm_bwd_quant_dual on h."""
+    _want(x, torch.bfloat16, 2, "x")
+    _want(gamma, torch.bfloat16, 1, "gamma")
+    _dense(gamma, "gamma"); _dense(q, "q"); _dense(s, "s")
+    M, H = x.shape
+    _shape(res, (M, H), torch.bfloat16, "res")
+    _shape(h, (M, H), torch.bfloat16, "h")
+    _shape(gamma, (H,), torch.bfloat16, "gamma")
+    _shape(q, (M, H), torch.uint8, "q")
+    _scales_1x128(s, _groups(H), M, "s")
+    _together((x, "x"), (res, "res"), (gamma, "gamma"), (h, "h"), (q, "q"), (s, "s"))
+    _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, x, _ptr(x), _ptr(res),
+         _ptr(gamma), M, H, _row_stride(x, "x"), _row_stride(res, "res"), float(eps), _ptr(h),
+         _row_stride(h, "h"), _ptr(q), _ptr(s), s.shape[1])
+
+
+def add_rmsnorm_quant_alloc(x, res, gamma, eps, stream=None):
+    """add_rmsnorm_quant into new tensors: (h, q, s)."""
+    M, H = x.shape
+    h = _empty((M, H), torch.bfloat16, x.device)
+    q = _empty((M, H), torch.uint8, x.device)
+    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device)
+    add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream)
+    return h, q, s
+
+
+def grouped_quant_weight_alloc(w, want_t=True, stream=None):
+    """The weights w BF16 [E,N,K] of E experts, quantized per 128x128 block by one
+    quant_weight_128x128 over the stacked [E*N,K] matrix: (qw [E,N,K], sw
+    [E,N/128,K/128], qwT [K,E,N] or None), the operands of the grouped products."""
+    _want(w, torch.bfloat16, 3, "w")
+    _dense(w, "w")
+    E, N, K = w.shape
+    if N % 128 or K % 128:
+        raise ValueError("w must be [E, N, K] with N and K multiples of 128, got %s" % (
+            tuple(w.shape),))
+    q, s, qT = quant_weight_alloc(w.view(E * N, K), want_t, stream)
+    return (q.view(E, N, K), s.view(E, N // 128, K // 128),
+            qT.view(K, E, N) if want_t else None)
+
+
+def _grouped_weight(qw, sw, offsets, name, N_at):
+    """Stacked weight codes (qw [E,N,K] with N_at = 1, qwT [K,E,N] with N_at = 2) and their
+    block scales sw [E,N/128,K/128], for offsets [E+1]; returns (E, N, K)."""
+    _want(qw, torch.uint8, 3, name)
+    _dense(qw, name)
+    E, N, K = qw.shape if N_at == 1 else (qw.shape[1], qw.shape[2], qw.shape[0])
+    if _offsets(offsets) != E:
+        raise ValueError("%s holds %d experts, offsets %d" % (name, E, offsets.numel() - 1))
+    _shape(sw, (E, _groups(N), _groups(K)), torch.float32, "sw")
+    _dense(sw, "sw")
+    return E, N, K
+
+
+def _grouped_rows(q, s, width, name_q, name_s):
+    """Row operand q [M,width] with its 1x128 scales; returns M."""
+    _want(q, torch.uint8, 2, name_q)
+    _dense(q, name_q); _dense(s, name_s)
+    M = q.shape[0]
+    _shape(q, (M, width), torch.uint8, name_q)
+    _scales_1x128(s, _groups(width), M, name_s)
+    return M
+
+
+def grouped_linear_fwd(qa, sa, qw, sw, offsets, y, stream=None):
+    """linear_fwd with one weight per expert: rows offsets[e] .. offsets[e+1]-1 of qa [M,K]
+    times qw[e] ([E,N,K], see grouped_quant_weight_alloc) -> the same rows of y BF16 [M,N].
+    Rows of no expert are left as they are. offsets: int32 [E+1] on the device."""
+    E, N, K = _grouped_weight(qw, sw, offsets, "qw", 1)
+    M = _grouped_rows(qa, sa, K, "qa", "sa")
+    _shape(y, (M, N), torch.bfloat16, "y")
+    _together((qa, "qa"), (sa, "sa"), (qw, "qw"), (sw, "sw"), (offsets, "offsets"), (y, "y"))
+    _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, qa, _ptr(qa), _ptr(sa),
+         sa.shape[1], _ptr(qw), _ptr(sw), _ptr(offsets), E, M, N, K, _ptr(y),
+         _row_stride(y, "y"))
+
+
+def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
+    """linear_dgrad with one weight per expert: qdy [M,N] x W[e] -> dx BF16 [M,K] (weights
+    transposed and stacked, qwT [K,E,N]). Rows of no expert are left as they are."""
+    E, N, K = _grouped_weight(qwT, sw, offsets, "qwT", 2)
+    M = _grouped_rows(qdy, sdy, N, "qdy", "sdy")
+    _shape(dx, (M, K), torch.bfloat16, "dx")
+    _together((qdy, "qdy"), (sdy, "sdy"), (qwT, "qwT"), (sw, "sw"), (offsets, "offsets"),
+              (dx, "dx"))
+    _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, qdy, _ptr(qdy),
+         _ptr(sdy), sdy.shape[1], _ptr(qwT), _ptr(sw), _ptr(offsets), E, M, N, K, _ptr(dx),
+         _row_stride(dx, "dx"))
+
+
+def _grouped_columns(qT, sT, rows, name_q, name_s):
+    """Transposed codes [rows,P] with their 128x1 scales [P/128,rows]; returns P."""
+    _want(qT, torch.uint8, 2, name_q)
+    _dense(qT, name_q); _dense(sT, name_s)
+    P = qT.shape[1]
+    if P % 128:
+        raise ValueError("%s must have a multiple of 128 columns, got %s" % (
+            name_q, tuple(qT.shape)))
+    _shape(qT, (rows, P), torch.uint8, name_q)
+    _shape(sT, (P // 128, rows), torch.float32, name_s)
+    return P
+
+
+def grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, stream=None):
+    """a6 with 128x1 groups that restart at each expert: dy BF16 [M,N] -> q_row [M,N], s_row
+    [N/128,lds] (both may be None) and q_colT [N,P], s_col [P/128,N], with
+    P >= grouped_padded_rows(M, E)."""
+    _want(dy, torch.bfloat16, 2, "dy")
+    E = _offsets(offsets)
+    M, N = dy.shape
+    lds_row = 0
+    if (q_row is None) != (s_row is None):
+        raise ValueError("q_row and s_row must be given together")
+    if q_row is not None:
+        _dense(q_row, "q_row"); _dense(s_row, "s_row")
+        _shape(q_row, (M, N), torch.uint8, "q_row")
+        _scales_1x128(s_row, _groups(N), M, "s_row")
+        lds_row = s_row.shape[1]
+    P = _grouped_columns(q_colT, s_col, N, "q_colT", "s_col")
+    _together((dy, "dy"), (offsets, "offsets"), (q_row, "q_row"), (s_row, "s_row"),
+              (q_colT, "q_colT"), (s_col, "s_col"))
+    _run(_lib.fp8q_grouped_transpose_quant_bf16, "fp8q_grouped_transpose_quant_bf16", stream, dy,
+         _ptr(dy), _ptr(offsets), E, M, N, _row_stride(dy, "dy"), _ptr(q_row), _ptr(s_row),
+         lds_row, _ptr(q_colT), _ptr(s_col), P)
+
+
+def grouped_transpose_quant_bf16_alloc(dy, offsets, want_row=True, stream=None):
+    """grouped_transpose_quant_bf16 into new tensors: (q_row, s_row, q_colT, s_col). Rows of
+    no expert and columns past the last group hold whatever the memory held."""
+    M, N = dy.shape
+    P = grouped_padded_rows(M, _offsets(offsets))
+    q_row = _empty((M, N), torch.uint8, dy.device) if want_row else None
+    s_row = _empty((_groups(N), lds_for(M)), torch.float32, dy.device) if want_row else None
+    q_colT = _empty((N, P), torch.uint8, dy.device)
+    s_col = _empty((P // 128, N), torch.float32, dy.device)
+    grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, stream)
+    return q_row, s_row, q_colT, s_col
+
+
+def grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream=None):
+    """a8 with 128x1 groups that restart at each expert: saved FP8 (q [M,K], s [K/128,lds])
+    -> qT [K,P], sT [P/128,K], with P >= grouped_padded_rows(M, E)."""
+    _want(q, torch.uint8, 2, "q")
+    E = _offsets(offsets)
+    K = q.shape[1]
+    M = _grouped_rows(q, s, K, "q", "s")
+    P = _grouped_columns(qT, sT, K, "qT", "sT")
+    _together((q, "q"), (s, "s"), (offsets, "offsets"), (qT, "qT"), (sT, "sT"))
+    _run(_lib.fp8q_grouped_transpose_quant_fp8, "fp8q_grouped_transpose_quant_fp8", stream, q,
+         _ptr(q), _ptr(s), _ptr(offsets), E, M, K, s.shape[1], _ptr(qT), _ptr(sT), P)
+
+
+def grouped_transpose_quant_fp8_alloc(q, s, offsets, stream=None):
+    """grouped_transpose_quant_fp8 into new tensors: (qT, sT)."""
+    M, K = q.shape
+    P = grouped_padded_rows(M, _offsets(offsets))
+    qT = _empty((K, P), torch.uint8, q.device)
+    sT = _empty((P // 128, K), torch.float32, q.device)
+    grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream)
+    return qT, sT
+
+
+def grouped_linear_wgrad(qdyT, sdy_c, qxT, sx_c, offsets, dw, stream=None):
+    """linear_wgrad per expert: dw[e] BF16 [N,K] = expert e's groups of qdyT [N,P] x qxT
+    [K,P]^T (the outputs of the grouped quantizers, one P for both); zeros for an expert
+    without rows. dw is [E,N,K], dense."""
+    _want(qdyT, torch.uint8, 2, "qdyT"); _want(qxT, torch.uint8, 2, "qxT")
+    N, K = qdyT.shape[0], qxT.shape[0]
+    if qxT.shape[1] != qdyT.shape[1]:
+        raise ValueError("qxT must have the columns of qdyT (%d), got %s" % (
+            qdyT.shape[1], tuple(qxT.shape)))
+    P = _grouped_columns(qdyT, sdy_c, N, "qdyT", "sdy_c")
+    _grouped_columns(qxT, sx_c, K, "qxT", "sx_c")
+    _want(dw, torch.bfloat16, 3, "dw")
+    E = dw.shape[0]
+    _shape(dw, (E, N, K), torch.bfloat16, "dw")
+    _dense(dw, "dw")
+    _offsets(offsets, E)
+    _together((qdyT, "qdyT"), (sdy_c, "sdy_c"), (qxT, "qxT"), (sx_c, "sx_c"),
+              (offsets, "offsets"), (dw, "dw"))
+    _run(_lib.fp8q_grouped_linear_wgrad, "fp8q_grouped_linear_wgrad", stream, qdyT, _ptr(qdyT),
+         _ptr(sdy_c), _ptr(qxT), _ptr(sx_c), _ptr(offsets), E, P, N, K, _ptr(dw), K)
 
 
 def debug_wait_timeout(limit_ns: int, stream=None) -> int:

@@ -10,7 +10,8 @@
 
 namespace fp8q {
 
-// Set by kernels when a bounded wait gives up (bit kErrTimeout).
+// Set by kernels when a bounded wait gives up (bit kErrTimeout) or group offsets had to
+// be clamped (bit kErrOffsets).
 __device__ unsigned g_device_error = 0;
 
 namespace {
@@ -158,6 +159,8 @@ extern "C" const char* fp8q_status_string(fp8q_status status) {
     case FP8Q_ERR_CUDA: return "FP8Q_ERR_CUDA: CUDA launch or runtime error";
     case FP8Q_ERR_TIMEOUT: return "FP8Q_ERR_TIMEOUT: a kernel gave up a bounded wait";
     case FP8Q_ERR_UNSUPPORTED: return "FP8Q_ERR_UNSUPPORTED: needs an sm_100 device";
+    case FP8Q_ERR_OFFSETS:
+      return "FP8Q_ERR_OFFSETS: group offsets decrease or leave the rows (clamped)";
     default: return "FP8Q_ERR_UNKNOWN";
   }
 }
@@ -178,11 +181,17 @@ extern "C" fp8q_status fp8q_device_error(void* stream, int clear) {
     if (cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
       return FP8Q_ERR_CUDA;
   }
-  return (v & kErrTimeout) ? FP8Q_ERR_TIMEOUT : FP8Q_OK;
+  if (v & kErrTimeout) return FP8Q_ERR_TIMEOUT;
+  return (v & kErrOffsets) ? FP8Q_ERR_OFFSETS : FP8Q_OK;
 }
 
 extern "C" fp8q_status fp8q_last_device_error(void* stream) {
   return fp8q_device_error(stream, 0);
+}
+
+extern "C" int64_t fp8q_grouped_padded_rows(int64_t M, int64_t E) {
+  if (M < 0 || E < 1 || E > kMaxExperts || M > 0x7FFFFFFF) return -1;
+  return grouped_padded_rows(M, E);
 }
 
 extern "C" fp8q_status fp8q_debug_wait_timeout(int64_t limit_ns, void* stream) {

@@ -19,6 +19,7 @@ namespace fp8q {
 // Device error word bits (the word itself lives in fp8q_api.cu; kernels get its
 // address as a parameter).
 constexpr unsigned kErrTimeout = 1u;
+constexpr unsigned kErrOffsets = 2u;  // group offsets out of order or out of range (clamped)
 
 // ---------------------------------------------------------------------------
 // Small helpers

@@ -56,6 +56,7 @@
 #include <mutex>
 
 #include "fp8q_device.cuh"
+#include "fp8q_grouped.cuh"
 #include "fp8q_host.h"
 
 namespace fp8q {
@@ -125,7 +126,8 @@ constexpr uint32_t kNumBars = 2 * kStages + 4 + 2 * kScSlotsMax + 1;
 constexpr uint32_t kOffMisc = kOffBars + kNumBars * 8;
 constexpr uint32_t kSmemUsed = kOffMisc + 16;
 constexpr size_t kSmemBytes = kSmemUsed + 1024;  // slack to align the base to 1024
-static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_100 CTA");
+constexpr size_t kGroupedSmemBytes = kSmemBytes + group_table_bytes(kMaxExperts);
+static_assert(kGroupedSmemBytes <= 232448 && kSmemUsed % 4 == 0, "shared memory budget of one sm_100 CTA");
 static_assert(kOffOut % 1024 == 0, "TMA store boxes need 1024-byte alignment");
 
 struct GemmParams {
@@ -139,6 +141,12 @@ struct GemmParams {
   int64_t ldy;
   unsigned* err;
   uint64_t wait_limit_ns;
+  // grouped calls (one weight per expert), see GroupTile
+  const int32_t* offsets;
+  int32_t experts;
+  int32_t limit;             // rows (forward, DGrad) / 128-row groups (WGrad) that exist
+  int32_t bx_step, by_step;  // an expert's step in B's tensor map (reduction, rows)
+  int64_t sb_se;             // and in the block scales
 };
 
 // Tile order. Within a group of `group` consecutive column panels (row panels with
@@ -164,6 +172,77 @@ __device__ __forceinline__ void tile_coords(int t, const GemmParams& p, int& mb,
   nb = p.swap ? y : x;
 }
 
+// One tile of a grouped call.
+//
+// Forward and DGrad: row blocks of 256 rows per expert, the first one starting at the
+// expert's first row rounded down to a multiple of 4 (the row scales come by tensor copy,
+// whose innermost coordinate must be a multiple of 16 bytes); rows of other experts inside
+// a block are computed and not stored. Experts without rows have no tiles. Within an
+// expert the tiles walk 8 column panels per row block, as in tile_coords.
+// WGrad: every expert has all N/256 x K/256 tiles of its dW (an expert without rows is
+// written as zeros) and its own part of the reduction, the 128-row groups first[e] ..
+// first[e + 1] - 1 of the transposed operands.
+struct GroupTile {
+  int row0;      // first A row of the pair's tile (token row; WGrad: row n of dY^T)
+  int lo, hi;    // rows of A that are the tile's own
+  int out_row0;  // row0's row in the output
+  int nb;        // column panel
+  int kblocks;   // slices of the reduction
+  int ax, bx;    // reduction coordinate of slice 0 in A's and B's tensor maps
+  int by;        // B's first row in its tensor map
+  int slice0;    // first slice in the scale arrays
+  int64_t sb;    // expert's offset in the block scales
+};
+
+template <bool kCol>
+__device__ __forceinline__ int grouped_row_blocks(int lo, int hi) {
+  if (kCol) return (hi - lo + BK - 1) / BK;
+  return hi > lo ? (hi - (lo & ~3) + kPairM - 1) / kPairM : 0;
+}
+
+template <bool kCol>
+__device__ __forceinline__ GroupTile grouped_tile(int t, const GemmParams& p, const int* off,
+                                                  const int* first) {
+  GroupTile g;
+  if (kCol) {
+    const int per = p.mblocks * p.nblocks;
+    const int e = t / per;
+    int mb;
+    tile_coords(t - e * per, p, mb, g.nb);
+    const int g0 = min(first[e], p.limit), g1 = min(first[e + 1], p.limit);
+    g.row0 = mb * kPairM;
+    g.lo = 0;
+    g.hi = p.M;
+    g.out_row0 = e * p.M + g.row0;
+    g.kblocks = g1 - g0;
+    g.ax = g.bx = g0 * BK;
+    g.by = 0;
+    g.slice0 = g0;
+    g.sb = 0;
+  } else {
+    const int e = group_find(first, p.experts, t / p.nblocks);
+    const int mblocks = first[e + 1] - first[e];
+    const int w = t - first[e] * p.nblocks;
+    const int span = p.group * mblocks;
+    const int grp = w / span;
+    const int v = w - grp * span;
+    const int width = min(p.group, p.nblocks - grp * p.group);
+    const int mb = v / width;
+    g.nb = grp * p.group + v - mb * width;
+    g.lo = off[e];
+    g.hi = off[e + 1];
+    g.row0 = (g.lo & ~3) + mb * kPairM;
+    g.out_row0 = g.row0;
+    g.kblocks = p.kblocks;
+    g.ax = 0;
+    g.bx = e * p.bx_step;
+    g.by = e * p.by_step;
+    g.slice0 = 0;
+    g.sb = e * p.sb_se;
+  }
+  return g;
+}
+
 // Wait used while winding down after a give-up: ignores the abort flag, still bounded.
 __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const uint32_t a = smem_u32(bar);
@@ -175,7 +254,8 @@ __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity, 
 
 // kAccF32: instead of storing BF16, add the fp32 accumulator into an fp32 output
 // (out += A x B^T) by TMA reduce-add of 32 x 32 boxes.
-template <bool kColScaleB, bool kAccF32 = false>
+// kGrouped: one weight per expert over ragged row groups (GroupTile).
+template <bool kColScaleB, bool kAccF32 = false, bool kGrouped = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -227,13 +307,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmY);
     if (kColScaleB) prefetch_tensormap(&tmSB);
   }
+  if constexpr (kGrouped) {
+    int* off = reinterpret_cast<int*>(smem + kSmemUsed);
+    group_table_fill(off, off + p.experts + 1, p.offsets, p.experts,
+                     kColScaleB ? 0x7FFFFFFF - BK : p.limit, p.err,
+                     grouped_row_blocks<kColScaleB>);
+    __syncwarp();
+    // WGrad: the last group must lie inside the transposed operands
+    if (kColScaleB && threadIdx.x == 0 && blockIdx.x == 0 && off[2 * p.experts + 1] > p.limit)
+      atomicOr(p.err, kErrOffsets);
+    __syncwarp();
+  }
   if (warp == 1) tmem_alloc_pair<kTmemCols>(tmem_slot);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.err, p.wait_limit_ns};
-  const int num_tiles = p.mblocks * p.nblocks;
+  int* const goff = reinterpret_cast<int*>(smem + kSmemUsed);
+  int* const gfirst = goff + p.experts + 1;
+  const int num_tiles = !kGrouped    ? p.mblocks * p.nblocks
+                        : kColScaleB ? p.experts * p.mblocks * p.nblocks
+                                     : gfirst[p.experts] * p.nblocks;
 
   if (warp < 4) {
    // Each role's code sits inside the branch of its register budget, so that the
@@ -247,23 +342,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t issued = 0, par = 0, sc_issued = 0, sc_par = 0;
       bool ok = true;
       for (int t = pair; ok && t < num_tiles; t += npairs) {
-        int mb, nb;
-        tile_coords(t, p, mb, nb);
-        const int row0 = mb * kPairM + static_cast<int>(rank) * BM;
-        const int brow0 = nb * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        [[maybe_unused]] int mb = 0, nb;
+        [[maybe_unused]] GroupTile g{};
+        if constexpr (kGrouped) {
+          g = grouped_tile<kColScaleB>(t, p, goff, gfirst);
+          nb = g.nb;
+        } else {
+          tile_coords(t, p, mb, nb);
+        }
+        const int row0 = (kGrouped ? g.row0 : mb * kPairM) + static_cast<int>(rank) * BM;
+        const int brow0 = (kGrouped ? g.by : 0) + nb * BN + static_cast<int>(rank) * (BN / 2);
+        const int ax = kGrouped ? g.ax : 0, bx = kGrouped ? g.bx : 0;
+        const int slice0 = kGrouped ? g.slice0 : 0;
+        const int kblocks = kGrouped ? g.kblocks : p.kblocks;
+        for (int kb = 0; kb < kblocks; ++kb) {
           if (!mbar_wait(empty + stage, phase ^ 1, ctl)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * kStageBytes);
           const uint32_t leader_full = cluster_addr(full + stage, 0);
-          tma_load_2d_pair(smem + kOffA(stage), &tmA, kb * BK, row0, leader_full);
-          tma_load_2d_pair(smem + kOffB(stage), &tmB, kb * BK, brow0, leader_full);
+          tma_load_2d_pair(smem + kOffA(stage), &tmA, ax + kb * BK, row0, leader_full);
+          tma_load_2d_pair(smem + kOffB(stage), &tmB, bx + kb * BK, brow0, leader_full);
           issued |= 1u << stage;
           par = (par & ~(1u << stage)) | (phase << stage);
           if (kb % sc_batch<kColScaleB>() == 0) {  // the scales of slices kb .. kb + batch - 1
             if (!mbar_wait(sempty + sci, scph ^ 1, ctl)) { ok = false; break; }
             mbar_arrive_expect_tx(sfull + sci, sc_a_bytes<kColScaleB>() + sc_b_bytes<kColScaleB>());
-            tma_load_2d(smem + off_sc_a<kColScaleB>(sci), &tmSA, row0, kb, sfull + sci);
-            if (kColScaleB) tma_load_2d(smem + off_sc_b<kColScaleB>(sci), &tmSB, nb * BN, kb, sfull + sci);
+            tma_load_2d(smem + off_sc_a<kColScaleB>(sci), &tmSA, row0, slice0 + kb, sfull + sci);
+            if (kColScaleB) tma_load_2d(smem + off_sc_b<kColScaleB>(sci), &tmSB, nb * BN, slice0 + kb, sfull + sci);
             sc_issued |= 1u << sci;
             sc_par = (sc_par & ~(1u << sci)) | (scph << sci);
             if (++sci == sc_slots<kColScaleB>()) { sci = 0; scph ^= 1; }
@@ -290,7 +394,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t stage = 0, phase = 0, it = 0;
       bool ok = true;
       for (int t = pair; ok && t < num_tiles; t += npairs) {
-        for (int kb = 0; ok && kb < p.kblocks; ++kb) {
+        const int kblocks =
+            kGrouped && kColScaleB ? grouped_tile<kColScaleB>(t, p, goff, gfirst).kblocks : p.kblocks;
+        for (int kb = 0; ok && kb < kblocks; ++kb) {
           const uint32_t buf = it & 1u, tph = (it >> 1) & 1u;
           if (issuers<kColScaleB>() == 2 && buf != issuer) {  // the other issuer's slice
             if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -336,15 +442,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t it = 0, sci = 0, scph = 0;
     bool ok = true, stored = false;
     for (int t = pair; ok && t < num_tiles; t += npairs) {
-      int mb, nb;
-      tile_coords(t, p, mb, nb);
-      const int row0 = mb * kPairM + static_cast<int>(rank) * BM;
+      [[maybe_unused]] int mb = 0, nb;
+      [[maybe_unused]] GroupTile g{};
+      if constexpr (kGrouped) {
+        g = grouped_tile<kColScaleB>(t, p, goff, gfirst);
+        nb = g.nb;
+      } else {
+        tile_coords(t, p, mb, nb);
+      }
+      const int row0 = (kGrouped ? g.row0 : mb * kPairM) + static_cast<int>(rank) * BM;
+      const int kblocks = kGrouped ? g.kblocks : p.kblocks;
       const int col_lo = nb * BN + 128 * half;  // tile columns of acc[0..63]
       const int col_hi = col_lo + 64;           // of acc[64..127]
       // a ragged N (a multiple of 16) ends inside a box: the tensor store clips it
       const bool lo_ok = col_lo < p.N;
       const bool hi_ok = col_hi < p.N;
-      const float* sbp = kColScaleB ? nullptr : p.sb + static_cast<int64_t>(col_lo / 128) * p.sb_sj;
+      const float* sbp = kColScaleB ? nullptr
+                                    : p.sb + (kGrouped ? g.sb : 0) + static_cast<int64_t>(col_lo / 128) * p.sb_sj;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
@@ -352,11 +466,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // next 32 are fetched 16 slices ahead (a global load per slice, even prefetched one
       // slice ahead, measured ~10 % slower)
       auto sb_fetch = [&](int kk) -> float {
-        return (!kColScaleB && lo_ok && kk < p.kblocks) ? __ldg(sbp + static_cast<int64_t>(kk) * p.sb_sr)
+        return (!kColScaleB && lo_ok && kk < kblocks) ? __ldg(sbp + static_cast<int64_t>(kk) * p.sb_sr)
                                                         : 0.0f;
       };
       float sbv = sb_fetch(lane), sbx = 0.0f;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = 0; kb < kblocks; ++kb) {
         const int j = kb % sc_batch<kColScaleB>();  // slice within its scale batch
         if (!kColScaleB) {
           if ((kb & 31) == 16) sbx = sb_fetch(kb + 16 + lane);
@@ -442,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive(tempty + buf);
           else mbar_arrive_cluster(tempty_leader0 + buf * 8);
         }
-        if (j == sc_batch<kColScaleB>() - 1 || kb == p.kblocks - 1) {
+        if (j == sc_batch<kColScaleB>() - 1 || kb == kblocks - 1) {
           mbar_arrive(sempty + sci);
           if (++sci == sc_slots<kColScaleB>()) { sci = 0; scph ^= 1; }
         }
@@ -452,7 +566,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // epilogue: BF16 rows into this warp's two swizzled 32 x 64 boxes, then TMA stores
       // (fp32 accumulate: four 32 x 32 boxes, two at a time, added by TMA reduce)
       const int wrow0 = row0 + wq * 32;
-      if (wrow0 < p.M && lo_ok) {
+      if constexpr (kGrouped && !kColScaleB) {
+        // a box with rows of other experts (or of nobody): each lane stores its own row
+        if (lo_ok && wrow0 < g.hi && wrow0 + 32 > g.lo && (wrow0 < g.lo || wrow0 + 32 > g.hi)) {
+          const int r = wrow0 + lane;
+          if (r >= g.lo && r < g.hi) {
+            uint16_t* dst = p.y + static_cast<int64_t>(r) * p.ldy + col_lo;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float* a = acc + c * 8;
+              *reinterpret_cast<uint4*>(dst + c * 8) =
+                  make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                             pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+            }
+          }
+          continue;
+        }
+      }
+      const bool rows_ok = !kGrouped    ? wrow0 < p.M
+                           : kColScaleB ? wrow0 < g.hi
+                                        : wrow0 >= g.lo && wrow0 + 32 <= g.hi;
+      const int out_row = kGrouped ? g.out_row0 + (wrow0 - g.row0) : wrow0;
+      if (rows_ok && lo_ok) {
         if constexpr (kAccF32) {
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {  // tile columns col_lo (hh = 0) / col_hi, 64 each
@@ -491,8 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0 && (hh == 0 || hi_ok)) {
               const int cb = hh ? col_hi : col_lo;
-              tma_reduce_add_2d(&tmY, out0, cb, wrow0);
-              if (cb + 32 < p.N) tma_reduce_add_2d(&tmY, out1, cb + 32, wrow0);  // ragged N
+              tma_reduce_add_2d(&tmY, out0, cb, out_row);
+              if (cb + 32 < p.N) tma_reduce_add_2d(&tmY, out1, cb + 32, out_row);  // ragged N
               tma_store_commit();
             }
             stored = true;
@@ -536,8 +671,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tmY, out0, col_lo, wrow0);
-            if (hi_ok) tma_store_2d(&tmY, out1, col_hi, wrow0);
+            tma_store_2d(&tmY, out0, col_lo, out_row);
+            if (hi_ok) tma_store_2d(&tmY, out1, col_hi, out_row);
             tma_store_commit();
           }
           stored = true;
@@ -560,8 +695,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // budget of the hand-over, and find how many CTA pairs can be resident at once (pairs
 // are placed within one GPC, so this can be below half the SM count). Returns that
 // number, or 0 on failure (the reason is in fp8q_last_error_message).
-template <bool kCol, bool kAcc = false>
+template <bool kCol, bool kAcc = false, bool kGrouped = false>
 int kernel_setup() {
+  constexpr size_t kSmem = kGrouped ? kGroupedSmemBytes : kSmemBytes;
   // written once per device under the lock; host threads may launch concurrently
   static std::atomic<int> pairs_for_device[64];
   static std::mutex mu;
@@ -571,8 +707,8 @@ int kernel_setup() {
   std::lock_guard<std::mutex> lock(mu);
   if (const int known = pairs_for_device[dev].load(std::memory_order_relaxed)) return known;
   const cudaError_t e = cudaFuncSetAttribute(
-      gemm_kernel<kCol, kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(kSmemBytes));
+      gemm_kernel<kCol, kAcc, kGrouped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      static_cast<int>(kSmem));
   if (e != cudaSuccess) {
     set_last_error("cudaFuncSetAttribute(gemm max dynamic smem)", e);
     cudaGetLastError();
@@ -581,7 +717,7 @@ int kernel_setup() {
   // The register hand-over inside the kernel waits until the block's launch allocation
   // covers the new budgets; refuse to launch a build whose allocation would not.
   cudaFuncAttributes attr;
-  const cudaError_t ea = cudaFuncGetAttributes(&attr, gemm_kernel<kCol, kAcc>);
+  const cudaError_t ea = cudaFuncGetAttributes(&attr, gemm_kernel<kCol, kAcc, kGrouped>);
   if (ea != cudaSuccess) {
     set_last_error("cudaFuncGetAttributes(gemm)", ea);
     cudaGetLastError();
@@ -596,7 +732,7 @@ int kernel_setup() {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 74, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = kSmem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
@@ -606,7 +742,7 @@ int kernel_setup() {
   cfg.numAttrs = 1;
   int clusters = 0;
   const cudaError_t eo =
-      cudaOccupancyMaxActiveClusters(&clusters, gemm_kernel<kCol, kAcc>, &cfg);
+      cudaOccupancyMaxActiveClusters(&clusters, gemm_kernel<kCol, kAcc, kGrouped>, &cfg);
   if (eo != cudaSuccess || clusters <= 0) {
     set_last_error("cudaOccupancyMaxActiveClusters(gemm)", eo != cudaSuccess ? eo : cudaErrorInvalidConfiguration);
     cudaGetLastError();
@@ -650,7 +786,7 @@ fp8q_status launch_gemm(const uint8_t* A, const uint8_t* B, int64_t Mg, int64_t 
   const int max_pairs = kernel_setup<kCol, kAcc>();
   if (max_pairs <= 0) return FP8Q_ERR_CUDA;
 
-  GemmParams p;
+  GemmParams p = {};
   p.M = static_cast<int32_t>(Mg);
   p.N = static_cast<int32_t>(Ng);
   p.K = static_cast<int32_t>(Kg);
@@ -681,6 +817,88 @@ fp8q_status launch_gemm(const uint8_t* A, const uint8_t* B, int64_t Mg, int64_t 
   gemm_kernel<kCol, kAcc><<<grid, kThreads, kSmemBytes, stream>>>(tmA, tmB, tmSA, tmSB,
                                                                            tmY, p);
   return launch_status("gemm_kernel launch");
+}
+
+// The products of a grouped call on the pair kernel. Forward / DGrad (kCol false):
+// A [rows][Kg] and out [rows][Ng] hold the experts' rows one after the other, B is one
+// tensor map over all experts' weights (b_inner x b_outer bytes) in which expert e starts
+// at (e * bx_step, e * by_step), its block scales at sb + e * sb_se. WGrad (kCol true):
+// A [Mg][P] and B [Ng][P] hold the experts' 128-row groups one after the other along P,
+// out [E * Mg][Ng] the experts' products.
+struct GroupedGemm {
+  const uint8_t *A, *B;
+  int64_t rows;  // token rows (forward, DGrad) / P (WGrad)
+  int64_t E, Mg, Ng, Kg;
+  int64_t b_inner, b_outer, bx_step, by_step;
+  const float* sa;
+  int64_t ldsa;
+  const float* sb;
+  int64_t sb_sj, sb_sr, sb_se;
+  const float* sbcol;
+  const int32_t* offsets;
+  void* y;
+  int64_t ldy;
+};
+
+template <bool kCol>
+fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
+  if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
+  const int64_t a_rows = kCol ? g.Mg : g.rows;       // rows of A
+  const int64_t a_inner = kCol ? g.rows : g.Kg;      // and their length
+  const int64_t out_rows = kCol ? g.E * g.Mg : g.rows;
+  const int64_t slices = a_inner / BK;
+  const int64_t nblocks = (g.Ng + BN - 1) / BN;
+  // row blocks at most: each expert with rows adds a partial block and up to 3 rows
+  const int64_t mblocks = kCol ? (g.Mg + kPairM - 1) / kPairM
+                               : (g.rows + (kPairM + 2) * std::min(g.E, g.rows)) / kPairM;
+  const int64_t tiles = mblocks * nblocks * (kCol ? g.E : 1);
+  if (tiles > 0x7FFFFFFF || out_rows > 0x7FFFFFFF || g.b_inner > 0x7FFFFFFF ||
+      g.b_outer > 0x7FFFFFFF || a_inner > 0x7FFFFFFF)
+    return FP8Q_ERR_SHAPE;
+  CUtensorMap tmA, tmB, tmSA, tmSB, tmY;
+  bool ok = encode_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.A, a_inner, a_rows, a_inner, BK,
+                           BM, CU_TENSOR_MAP_SWIZZLE_128B) &&
+            encode_tmap_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.B, g.b_inner, g.b_outer,
+                           g.b_inner, BK, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+            encode_tmap_2d(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.y, g.Ng, out_rows, g.ldy * 2,
+                           64, 32, CU_TENSOR_MAP_SWIZZLE_128B) &&
+            encode_tmap_2d(&tmSA, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.sa, a_rows, slices,
+                           g.ldsa * 4, BM, sc_batch<kCol>(), CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (ok && kCol)
+    ok = encode_tmap_2d(&tmSB, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.sbcol, g.Ng, slices, g.Ng * 4,
+                        BN, sc_batch<kCol>(), CU_TENSOR_MAP_SWIZZLE_NONE);
+  else
+    tmSB = tmSA;
+  if (!ok) return FP8Q_ERR_UNSUPPORTED;
+  const int max_pairs = kernel_setup<kCol, false, true>();
+  if (max_pairs <= 0) return FP8Q_ERR_CUDA;
+
+  GemmParams p = {};
+  p.M = static_cast<int32_t>(kCol ? g.Mg : g.rows);
+  p.N = static_cast<int32_t>(g.Ng);
+  p.K = static_cast<int32_t>(g.Kg);
+  p.mblocks = static_cast<int32_t>(mblocks);
+  p.nblocks = static_cast<int32_t>(nblocks);
+  p.kblocks = static_cast<int32_t>(slices);
+  p.group = static_cast<int32_t>(std::min<int64_t>(8, nblocks));
+  p.sb = g.sb;
+  p.sb_sj = g.sb_sj;
+  p.sb_sr = g.sb_sr;
+  p.sb_se = g.sb_se;
+  p.y = static_cast<uint16_t*>(g.y);
+  p.ldy = g.ldy;
+  p.offsets = g.offsets;
+  p.experts = static_cast<int32_t>(g.E);
+  p.limit = static_cast<int32_t>(kCol ? slices : g.rows);
+  p.bx_step = static_cast<int32_t>(g.bx_step);
+  p.by_step = static_cast<int32_t>(g.by_step);
+  p.err = device_error_word();
+  p.wait_limit_ns = kWaitLimitNs;
+  if (!p.err) return FP8Q_ERR_CUDA;
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, max_pairs));
+  gemm_kernel<kCol, false, true>
+      <<<grid, kThreads, kGroupedSmemBytes, stream>>>(tmA, tmB, tmSA, tmSB, tmY, p);
+  return launch_status("grouped gemm_kernel launch");
 }
 
 }  // namespace
@@ -758,4 +976,75 @@ extern "C" fp8q_status fp8q_linear_wgrad_acc_f32(const uint8_t* qdyT, const floa
   // as fp8q_linear_wgrad, with dw += the fp32 accumulator instead of dw = bf16(it)
   return launch_gemm<true, true>(qdyT, qxT, N, K, M, sdy_c, N, nullptr, 0, 0, sx_c, dw,
                                         lddw, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8q_status fp8q_grouped_linear_fwd(const uint8_t* qa, const float* sa, int64_t ldsa,
+                                               const uint8_t* qw, const float* sw,
+                                               const int32_t* offsets, int64_t E, int64_t M,
+                                               int64_t N, int64_t K, uint16_t* y, int64_t ldy,
+                                               void* stream) {
+  if (E < 1 || E > kMaxExperts || M < 0 || N <= 0 || K <= 0 || N % 128 || K % 128 || ldsa < M ||
+      ldy < N)
+    return FP8Q_ERR_SHAPE;
+  if (M == 0) return FP8Q_OK;
+  if (!qa || !sa || !qw || !sw || !offsets || !y) return FP8Q_ERR_NULL;
+  if (!aligned16(qa) || !aligned16(sa) || !aligned16(qw) || !aligned16(sw) || !aligned16(y) ||
+      !aligned4(offsets) || ldsa % 4 || ldy % 8)
+    return FP8Q_ERR_ALIGN;
+  // B = the stacked weights [E * N][K]; block scale of (e, n, slice r) =
+  // sw[e * NB * KB + (n/128) * KB + r]
+  const int64_t NB = N / 128, KB = K / 128;
+  const GroupedGemm g = {qa, qw, M,  E,  M,  N,       K,       K,       E * N,  0,
+                         N,  sa, ldsa, sw, KB, 1, NB * KB, nullptr, offsets, y, ldy};
+  return launch_grouped<false>(g, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8q_status fp8q_grouped_linear_dgrad(const uint8_t* qdy, const float* sdy,
+                                                 int64_t ldsdy, const uint8_t* qwT,
+                                                 const float* sw, const int32_t* offsets,
+                                                 int64_t E, int64_t M, int64_t N, int64_t K,
+                                                 uint16_t* dx, int64_t lddx, void* stream) {
+  if (E < 1 || E > kMaxExperts || M < 0 || N <= 0 || K <= 0 || N % 128 || K % 128 || ldsdy < M ||
+      lddx < K)
+    return FP8Q_ERR_SHAPE;
+  if (M == 0) return FP8Q_OK;
+  if (!qdy || !sdy || !qwT || !sw || !offsets || !dx) return FP8Q_ERR_NULL;
+  if (!aligned16(qdy) || !aligned16(sdy) || !aligned16(qwT) || !aligned16(sw) || !aligned16(dx) ||
+      !aligned4(offsets) || ldsdy % 4 || lddx % 8)
+    return FP8Q_ERR_ALIGN;
+  // GEMM columns = K, reduction = N. B = the transposed stacked weights [K][E * N], expert
+  // e's slices from column e * N on; block scale of (e, k, slice r over n) =
+  // sw[e * NB * KB + r * KB + k/128]
+  const int64_t NB = N / 128, KB = K / 128;
+  const GroupedGemm g = {qdy, qwT, M,   E,     M,  K, N,  E * N,   K,       N, 0,
+                         sdy, ldsdy, sw, 1, KB, NB * KB, nullptr, offsets, dx, lddx};
+  return launch_grouped<false>(g, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8q_status fp8q_grouped_linear_wgrad(const uint8_t* qdyT, const float* sdy_c,
+                                                 const uint8_t* qxT, const float* sx_c,
+                                                 const int32_t* offsets, int64_t E, int64_t P,
+                                                 int64_t N, int64_t K, uint16_t* dw, int64_t lddw,
+                                                 void* stream) {
+  if (E < 1 || E > kMaxExperts || P < 0 || P % 128 || N <= 0 || K <= 0 || N % 128 || K % 128 ||
+      lddw < K)
+    return FP8Q_ERR_SHAPE;
+  if (!dw || (P > 0 && (!qdyT || !sdy_c || !qxT || !sx_c || !offsets))) return FP8Q_ERR_NULL;
+  if (!aligned16(dw) || lddw % 8 ||
+      (P > 0 && (!aligned16(qdyT) || !aligned16(sdy_c) || !aligned16(qxT) || !aligned16(sx_c) ||
+                 !aligned4(offsets))))
+    return FP8Q_ERR_ALIGN;
+  if (P == 0) {  // no rows at all: every dW is zero
+    if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
+    const cudaError_t e = cudaMemset2DAsync(dw, lddw * 2, 0, K * 2, E * N,
+                                            static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) return FP8Q_OK;
+    set_last_error("cudaMemset2DAsync (grouped wgrad without rows)", e);
+    cudaGetLastError();
+    return FP8Q_ERR_CUDA;
+  }
+  // GEMM rows = N, columns = K, reduction = expert e's groups along P
+  const GroupedGemm g = {qdyT, qxT, P, E, N, K, P, P, K, 0, 0, sdy_c, N, nullptr, 0, 0, 0, sx_c,
+                         offsets, dw, lddw};
+  return launch_grouped<true>(g, static_cast<cudaStream_t>(stream));
 }

@@ -29,6 +29,7 @@ bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
                     const uint64_t (&dims)[3], const uint64_t (&strides_bytes)[2],
                     const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Remembers the text of a failure for fp8q_last_error_message (thread-local).
@@ -47,6 +48,15 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Token batches up to this many rows take the skinny-M GEMM (forward and DGrad).
 constexpr int64_t kSkinnyMaxM = 256;
+
+// Most experts of a grouped call (their table sits in each CTA's shared memory).
+constexpr int64_t kMaxExperts = 1024;
+
+// Columns of the transposed arrays of a grouped call, at most: each of the at most
+// min(E, M) experts with rows fills its last 128-row group up.
+inline int64_t grouped_padded_rows(int64_t M, int64_t E) {
+  return 128 * ((M + 127 * (E < M ? E : M)) / 128);
+}
 
 // out [Mg][Ng] = A [Mg][Kg] x B [Ng][Kg]^T with per-row A scales sa[r*ldsa + i] and
 // per-128x128-block B scales sb[(j/128)*sb_sj + r*sb_sr], for Mg <= kSkinnyMaxM.

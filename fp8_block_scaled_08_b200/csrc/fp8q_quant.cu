@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include "fp8q_device.cuh"
+#include "fp8q_grouped.cuh"
 #include "fp8q_host.h"
 
 namespace fp8q {
@@ -895,6 +896,71 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_cta_kernel(
   }
 }
 
+// 16 bytes of an operand that the same call may also write (the residual stream in place):
+// an ordinary load, not the read-only path.
+__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// Two BF16 pairs added, each sum formed in fp32 and rounded to BF16.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  return pack_bf16x2(__fadd_rn(bf16_lo(a), bf16_lo(b)), __fadd_rn(bf16_hi(a), bf16_hi(b)));
+}
+__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
+                    add_bf16x2(a.w, b.w));
+}
+
+// Residual addition + RMSNorm + quantization, one CTA per row: h = bf16(x + res) is formed
+// in registers, stored, and normalized from there, so each of x, res and h crosses HBM
+// once. kChunks 16-byte chunks per thread (H <= 8 * kChunks * threads).
+template <int kChunks>
+__global__ void __launch_bounds__(kNormThreads) add_rmsnorm_quant_cta_kernel(
+    const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ gamma, int64_t M,
+    int64_t H, int64_t ldx, int64_t ldr, float eps, uint16_t* h, int64_t ldh,
+    uint8_t* __restrict__ q, float* __restrict__ s, int64_t lds) {
+  __shared__ double red[kNormThreads / 32];
+  extern __shared__ uint4 gamma_sm[];  // H BF16 values, shared by every row
+  const int tid = threadIdx.x;
+  const int lane = tid & 31, wid = tid >> 5;
+  const int64_t nch = H >> 3;
+  for (int64_t i = tid; i < nch; i += kNormThreads) gamma_sm[i] = ld_nc_v4(gamma + i * 8);
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+    uint4 raw[kChunks];
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int64_t c = tid + j * kNormThreads;
+      if (c < nch) {
+        raw[j] = add_bf16x8(ld_stream_v4(x + m * ldx + c * 8), ld_stream_v4(res + m * ldr + c * 8));
+        *reinterpret_cast<uint4*>(h + m * ldh + c * 8) = raw[j];
+      }
+    }
+    double ss = sum_squares<kChunks>(raw, tid, kNormThreads, nch);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(kFull, ss, off));
+    if (lane == 0) red[wid] = ss;
+    __syncthreads();
+    double tot = 0.0;
+#pragma unroll
+    for (int w = 0; w < kNormThreads / 32; ++w) tot = __dadd_rn(tot, red[w]);
+    const float r = rstd_from_ss(tot, H, eps);
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int64_t c0 = static_cast<int64_t>(j) * kNormThreads + (tid & ~31);
+      if (c0 >= nch) break;  // warp-uniform; lanes past nch (a partial group) hold zeros
+      const int64_t c = tid + j * kNormThreads;
+      norm_quant_chunk(raw[j], reinterpret_cast<const uint16_t*>(gamma_sm), c, c < nch, r,
+                       q + m * H, s, lds, m, lane);
+    }
+    __syncthreads();  // red is reused by the next row
+  }
+}
+
 // Lane-per-group RMSNorm + quantization (H a multiple of 128, at most 64 groups): a unit
 // is one row, staged whole by one tensor copy (a [M][G][128] view); consumer warp w takes
 // rows w, w + kConsumers, ... of the CTA's share. Lane l owns groups l, l + 32, ...: it
@@ -1073,6 +1139,16 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1) rmsnorm_lane_kernel(
 // ---------------------------------------------------------------------------
 constexpr int kTileElems = 128 * 128;
 
+// Arguments of a grouped tile kernel: the experts' row offsets (fp8q_grouped.cuh), the
+// length of a row of the transposed codes, and the row codes' address (the rows of a group
+// that ends inside a warp's box are stored one by one). Unused by the ungrouped kernels.
+struct TileGroups {
+  const int32_t* offsets;
+  int experts;
+  int64_t P;
+  uint8_t* q_row;
+};
+
 struct TileSmem {
   uint8_t* buf[2];
   uint64_t* bar;  // [2]
@@ -1173,6 +1249,11 @@ __device__ __forceinline__ void tile_cols_bf16(const uint16_t* Ts, float* red, b
 
 // Shared memory of the FP8 tile kernel (a8): two (16 KB codes + 512 B row scales) buffers.
 constexpr size_t kTileSmemFP8 = 1024 + 2 * (kTileElems + 512) + 4 * 128 * 4 + 64;
+// Grouped: 132 row scales, rounded up to the 128 bytes a tensor copy's destination needs.
+constexpr int kGroupedTileFP8 = kTileElems + 640;
+constexpr size_t grouped_tile_smem_fp8(int E) {
+  return 1024 + 2 * kGroupedTileFP8 + 4 * 128 * 4 + 64 + group_table_bytes(E);
+}
 
 __device__ __forceinline__ TileSmem carve_tiles(uint8_t* raw, int buf_bytes,
                                                int red_floats = 4 * 128) {
@@ -1890,12 +1971,18 @@ __device__ __forceinline__ void half_row_codes(const uint4 (&w)[8], const GroupS
   }
 }
 
-template <class Src, bool kRows>
+// Units of a grouped call: 128-row groups per expert (128x1 groups restart at each expert).
+__device__ __forceinline__ int groups_of_rows(int lo, int hi) { return (hi - lo + 127) >> 7; }
+
+// kGrouped: the 128-row blocks are the experts' groups; a group's last rows may belong to
+// the next expert: they count as zeros in the columns, and their row codes are not stored
+// here (they are rows of that expert's own groups).
+template <class Src, bool kRows, bool kGrouped = false>
 __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmD1,
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQT, Src src,
     int64_t M, int64_t N, float* __restrict__ s_row, int64_t lds_row, float* __restrict__ s_col,
-    unsigned* err, uint64_t limit_ns) {
+    unsigned* err, uint64_t limit_ns, const TileGroups grp) {
   using L = A6Layout<Src>;
   constexpr int kStages = L::kStages;
   constexpr uint32_t kStageBytes = L::kStageBytes;
@@ -1924,9 +2011,25 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
     *abort_flag = 0;
     fence_barrier_init();
   }
+  int* const goff = reinterpret_cast<int*>(abort_flag + 4);
+  int* const gfirst = goff + grp.experts + 1;
+  if constexpr (kGrouped)
+    group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
+                     groups_of_rows);
   __syncthreads();
   const int64_t NB = (N + 127) >> 7;
-  const int64_t tiles = ((M + 127) >> 7) * NB;
+  const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * NB;
+  // first row of row block mb, and one past its last row
+  auto block_rows = [&](int64_t mb, int64_t& r0, int64_t& r1) {
+    if constexpr (kGrouped) {
+      const int e = group_find(gfirst, grp.experts, static_cast<int>(mb));
+      r0 = goff[e] + 128 * (mb - gfirst[e]);
+      r1 = min(static_cast<int64_t>(goff[e + 1]), r0 + 128);
+    } else {
+      r0 = mb * 128;
+      r1 = M;
+    }
+  };
   if (warp == 16) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -1938,9 +2041,11 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         const uint32_t ph = static_cast<uint32_t>(i / kStages) & 1u;
         if (i >= kStages && !mbar_wait(empty + b, ph ^ 1u, ctl)) { ok = false; break; }
         const int64_t mb = t / NB, nb = t - mb * NB;
+        int64_t r0, r1;
+        block_rows(mb, r0, r1);
         mbar_arrive_expect_tx(full + b, kStageBytes);
         tma_load_2d(base + b * kStageBytes, &tmD, static_cast<int32_t>(nb * 128),
-                    static_cast<int32_t>(mb * 128), full + b);
+                    static_cast<int32_t>(r0), full + b);
         if (Src::kBoxes == 2)
           tma_load_2d(base + b * kStageBytes + kA6Tile, &tmD1, static_cast<int32_t>(nb * 128),
                       static_cast<int32_t>(mb * 128), full + b);
@@ -2005,15 +2110,26 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         __syncwarp();
       }
       half_row_codes(w, g, out + rl * 128 + hh * 64, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      const int64_t m0 = mb * 128 + warp * 16;
-      if (lane == 0) {
-        tma_store_2d(&tmQ, out, static_cast<int32_t>(nb * 128), static_cast<int32_t>(m0));
-        tma_store_commit();
+      int64_t r0, r1;
+      block_rows(mb, r0, r1);
+      const int64_t m0 = r0 + warp * 16;
+      if (!kGrouped || m0 + 16 <= r1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tmQ, out, static_cast<int32_t>(nb * 128), static_cast<int32_t>(m0));
+          tma_store_commit();
+        }
+        stored = true;
+      } else if (m0 + rl < r1) {  // the group ends inside this box: row by row
+        const int64_t col = nb * 128 + hh * 64;
+        const uint4* src_row = reinterpret_cast<const uint4*>(out + rl * 128 + hh * 64);
+        uint4* dst = reinterpret_cast<uint4*>(grp.q_row + (m0 + rl) * N + col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + 16 * j < N) dst[j] = src_row[j];  // N is a multiple of 16
       }
-      stored = true;
-      if (hh == 0 && m0 + rl < M) s_row[nb * lds_row + m0 + rl] = g.s;
+      if (hh == 0 && m0 + rl < r1) s_row[nb * lds_row + m0 + rl] = g.s;
     }
   } else {
     // ------------------------------------------------------------ 128x1 columns
@@ -2040,6 +2156,15 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
       uint32_t w[32];  // columns c0, c0 + 1 of rows 32 q4 + k
 #pragma unroll
       for (int k = 0; k < 32; ++k) w[k] = tw[k * 64];
+      if constexpr (kGrouped) {  // rows past the group's end
+        int64_t r0, r1;
+        block_rows(t / NB, r0, r1);
+        const int valid = static_cast<int>(r1 - r0) - q4 * 32;
+        if (valid < 32) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) w[k] = k < valid ? w[k] : 0u;
+        }
+      }
       uint32_t m0 = 0u, m1 = 0u;
 #pragma unroll
       for (int k = 0; k < 32; k += 2) {
@@ -2630,23 +2755,49 @@ __global__ void __launch_bounds__(256) dgamma_round_kernel(const unsigned long l
 // quot's q + (x - q s) y with y = fl32(1/s) and q = fl32(x y) is fl32(x / s) for every
 // x and s of fp32 without underflow (Markstein's theorem: y within half an ulp of 1/s,
 // q within one ulp of x/s, the residual exact by the FMA). Scales below 2^-80 divide.
+// kGrouped: the 128-row blocks are the experts' groups (they restart at each expert; rows
+// past a group's end count as zeros), and qT's rows are grp.P long. A group may start at
+// any row, so its row scales come as a copy of 132 from the multiple of 4 before it.
+template <bool kGrouped>
 __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmS, int64_t M,
     int64_t K, uint8_t* __restrict__ qT, float* __restrict__ sT, unsigned* err,
-    uint64_t limit_ns) {
+    uint64_t limit_ns, const TileGroups grp) {
   extern __shared__ uint8_t smem_raw[];
-  const TileSmem sm = carve_tiles(smem_raw, kTileElems + 512);
+  constexpr int kScRows = kGrouped ? 132 : 128;
+  const TileSmem sm = carve_tiles(smem_raw, kGrouped ? kGroupedTileFP8 : kTileElems + 512);
+  int* const goff = sm.flag + 4;
+  int* const gfirst = goff + grp.experts + 1;
+  if constexpr (kGrouped) {
+    group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
+                     groups_of_rows);
+    __syncthreads();
+  }
   __shared__ int abort_flag;
   const WaitCtl ctl{&abort_flag, err, limit_ns};
   if (threadIdx.x == 0) abort_flag = 0;
   const int64_t KB = (K + 127) >> 7;
-  const int64_t tiles = ((M + 127) >> 7) * KB;
+  const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * KB;
+  const int64_t P = kGrouped ? grp.P : M;
   const int tid = threadIdx.x;
+  // first row of row block mb, and (grouped) how many rows it has
+  auto block_rows = [&](int64_t mb, int& rows) -> int32_t {
+    if constexpr (kGrouped) {
+      const int e = group_find(gfirst, grp.experts, static_cast<int>(mb));
+      const int r0 = goff[e] + 128 * (static_cast<int>(mb) - gfirst[e]);
+      rows = min(128, goff[e + 1] - r0);
+      return r0;
+    } else {
+      rows = 128;
+      return static_cast<int32_t>(mb * 128);
+    }
+  };
   auto issue = [&](int b, int64_t t) {
-    const int32_t mx = static_cast<int32_t>((t / KB) * 128), kx = static_cast<int32_t>(t % KB);
-    mbar_arrive_expect_tx(sm.bar + b, kTileElems + 512);
+    int rows;
+    const int32_t mx = block_rows(t / KB, rows), kx = static_cast<int32_t>(t % KB);
+    mbar_arrive_expect_tx(sm.bar + b, kTileElems + 4 * kScRows);
     tma_load_2d(sm.buf[b], &tmQ, kx * 128, mx, sm.bar + b);
-    tma_load_2d(sm.buf[b] + kTileElems, &tmS, mx, kx, sm.bar + b);
+    tma_load_2d(sm.buf[b] + kTileElems, &tmS, kGrouped ? mx & ~3 : mx, kx, sm.bar + b);
   };
   tiles_prologue(sm, tiles, issue);
   const int cp = tid & 63, rq = tid >> 6;
@@ -2659,10 +2810,18 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const float* rsc = reinterpret_cast<const float*>(Tq + kTileElems);
     const int64_t mb = t / KB, kb = t % KB;
     float x0[32], x1[32];
+    int grows = 128;
+    if constexpr (kGrouped) rsc += block_rows(mb, grows) & 3;
 #pragma unroll
     for (int r4 = 0; r4 < 32; r4 += 4) {
-      const float4 sr4 = *reinterpret_cast<const float4*>(rsc + 32 * rq + r4);  // broadcast
-      const float sr[4] = {sr4.x, sr4.y, sr4.z, sr4.w};
+      float sr[4];
+      if constexpr (kGrouped) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sr[k] = rsc[32 * rq + r4 + k];  // broadcast
+      } else {
+        const float4 sr4 = *reinterpret_cast<const float4*>(rsc + 32 * rq + r4);  // broadcast
+        sr[0] = sr4.x; sr[1] = sr4.y; sr[2] = sr4.z; sr[3] = sr4.w;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = r4 + k;
@@ -2670,6 +2829,15 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
         const float2 d = e4m3x2_to_f32(two);
         x0[r] = __fmul_rn(sr[k], d.x);
         x1[r] = __fmul_rn(sr[k], d.y);
+      }
+    }
+    if constexpr (kGrouped) {
+      if (32 * rq + 32 > grows) {  // rows past the group's end
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+          x0[r] = 32 * rq + r < grows ? x0[r] : 0.0f;
+          x1[r] = 32 * rq + r < grows ? x1[r] : 0.0f;
+        }
       }
     }
     float c0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -2690,7 +2858,7 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const GroupScale g0 = group_scale_fma(a0), g1 = group_scale_fma(a1);
     const float s0 = g0.s, s1 = g1.s;
     // a partial tile (ragged M or K) arrived zero-filled; store only its valid part
-    const int rows = M - mb * 128 < 128 ? static_cast<int>(M - mb * 128) : 128;
+    const int rows = !kGrouped && M - mb * 128 < 128 ? static_cast<int>(M - mb * 128) : 128;
     const bool col_ok = kb * 128 + 2 * cp < K;  // K is even: the pair is in or out
     if (rq == 0 && col_ok)
       *reinterpret_cast<float2*>(sT + mb * K + kb * 128 + 2 * cp) = make_float2(s0, s1);
@@ -2717,9 +2885,9 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
         o1[k] = cvt_e4m3x4(t1[0], t1[1], t1[2], t1[3]);
       }
     }
-    uint8_t* dst = qT + (kb * 128) * M + mb * 128;
-    uint4* d0 = reinterpret_cast<uint4*>(dst + (2 * cp) * M + 32 * rq);
-    uint4* d1 = reinterpret_cast<uint4*>(dst + (2 * cp + 1) * M + 32 * rq);
+    uint8_t* dst = qT + (kb * 128) * P + mb * 128;
+    uint4* d0 = reinterpret_cast<uint4*>(dst + (2 * cp) * P + 32 * rq);
+    uint4* d1 = reinterpret_cast<uint4*>(dst + (2 * cp + 1) * P + 32 * rq);
     if (col_ok && 32 * rq < rows) {  // rows is a multiple of 16
       d0[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
       d1[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
@@ -3165,12 +3333,14 @@ extern "C" fp8q_status fp8q_transpose_quant_bf16(const uint16_t* dy, int64_t M, 
     static std::atomic<int> occ[64];
     const int per_sm = resident_ctas(a6_tile_kernel<TileGrad, true>, kA6Threads, kSmem, occ);
     a6_tile_kernel<TileGrad, true><<<grid_for(tiles, per_sm), kA6Threads, kSmem, st>>>(
-        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs);
+        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs,
+        TileGroups{});
   } else {
     static std::atomic<int> occ[64];
     const int per_sm = resident_ctas(a6_tile_kernel<TileGrad, false>, kA6Threads, kSmem, occ);
     a6_tile_kernel<TileGrad, false><<<grid_for(tiles, per_sm), kA6Threads, kSmem, st>>>(
-        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs);
+        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs,
+        TileGroups{});
   }
   return launch_status("transpose_quant_bf16 launch");
 }
@@ -3194,10 +3364,10 @@ extern "C" fp8q_status fp8q_transpose_quant_fp8(const uint8_t* q, const float* s
   unsigned* err = device_error_word();
   if (!err) return FP8Q_ERR_CUDA;
   static std::atomic<int> occ[64];
-  const int per_sm = resident_ctas(transpose_quant_fp8_kernel, 256, kTileSmemFP8, occ);
-  transpose_quant_fp8_kernel<<<grid_for(((M + 127) / 128) * KB, per_sm), 256, kTileSmemFP8,
+  const int per_sm = resident_ctas(transpose_quant_fp8_kernel<false>, 256, kTileSmemFP8, occ);
+  transpose_quant_fp8_kernel<false><<<grid_for(((M + 127) / 128) * KB, per_sm), 256, kTileSmemFP8,
                                static_cast<cudaStream_t>(stream)>>>(tmq, tms, M, K, qT, sT, err,
-                                                                    kWaitLimitNs);
+                                                                    kWaitLimitNs, TileGroups{});
   return launch_status("transpose_quant_fp8 launch");
 }
 
@@ -3237,7 +3407,8 @@ extern "C" fp8q_status fp8q_rmsnorm_quant_dual(const uint16_t* x, const uint16_t
   static std::atomic<int> occ[64];
   const int per_sm = resident_ctas(kern, kA6Threads, kSmem, occ);
   kern<<<grid_for((M / 128) * (H / 128), per_sm), kA6Threads, kSmem, st>>>(
-      tmx, tmx, tmq, tmqt, TileRms{rstd, gamma}, M, H, s_row, lds_row, s_col, err, kWaitLimitNs);
+      tmx, tmx, tmq, tmqt, TileRms{rstd, gamma}, M, H, s_row, lds_row, s_col, err, kWaitLimitNs,
+      TileGroups{});
   return launch_status("rmsnorm_quant_dual launch");
 }
 
@@ -3366,4 +3537,119 @@ extern "C" fp8q_status fp8q_rmsnorm_bwd_quant_dual(
   if (s1 != FP8Q_OK) return s1;
   dgamma_round_kernel<<<static_cast<int>((H + 255) / 256), 256, 0, st>>>(bins, H, dgamma);
   return launch_status("dgamma_round launch");
+}
+
+// Two row-strided BF16 matrices of M rows x H columns: the same memory with the same
+// strides (an operand updated in place), or apart.
+static bool same_or_apart(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int64_t M,
+                          int64_t H) {
+  if (a == b) return lda == ldb || M == 1;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + 2 * ((M - 1) * lda + H), b1 = b0 + 2 * ((M - 1) * ldb + H);
+  if (a1 <= b0 || b1 <= a0) return true;
+  if (lda != ldb) return false;
+  // interleaved columns of one wider tensor: the distance within a row keeps them apart
+  const int64_t d = static_cast<int64_t>(a0 < b0 ? b0 - a0 : a0 - b0) / 2 % lda;
+  return d >= H && lda - d >= H;
+}
+
+extern "C" fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t* res,
+                                              const uint16_t* gamma, int64_t M, int64_t H,
+                                              int64_t ldx, int64_t ldres, float eps, uint16_t* h,
+                                              int64_t ldh, uint8_t* q, float* s, int64_t lds,
+                                              void* stream) {
+  if (!x || !res || !gamma || !h || !q || !s) return FP8Q_ERR_NULL;
+  if (M <= 0 || H <= 0 || H % 16 || H > 8 * kNormMaxChunks * kNormThreads || ldx < H ||
+      ldres < H || ldh < H || lds < M || lds % 4 || !(eps >= 0.0f))
+    return FP8Q_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(res) || !aligned16(gamma) || !aligned16(h) || !aligned16(q) ||
+      !aligned16(s) || ldx % 8 || ldres % 8 || ldh % 8)
+    return FP8Q_ERR_ALIGN;
+  if (!same_or_apart(h, ldh, x, ldx, M, H) || !same_or_apart(h, ldh, res, ldres, M, H))
+    return FP8Q_ERR_SHAPE;
+  const int sms = sm100_sm_count();
+  if (!sms) return FP8Q_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t gsm = static_cast<size_t>(H) * 2;  // gamma in shared memory
+  const int64_t grid = M < static_cast<int64_t>(sms) * 64 ? M : static_cast<int64_t>(sms) * 64;
+  auto kern = H <= 2 * 8 * kNormThreads   ? add_rmsnorm_quant_cta_kernel<2>
+              : H <= 4 * 8 * kNormThreads ? add_rmsnorm_quant_cta_kernel<4>
+                                          : add_rmsnorm_quant_cta_kernel<kNormMaxChunks>;
+  kern<<<static_cast<int>(grid), kNormThreads, gsm, st>>>(x, res, gamma, M, H, ldx, ldres, eps, h,
+                                                          ldh, q, s, lds);
+  return launch_status("add_rmsnorm_quant launch");
+}
+
+extern "C" fp8q_status fp8q_grouped_transpose_quant_bf16(
+    const uint16_t* dy, const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t lddy,
+    uint8_t* q_row, float* s_row, int64_t lds_row, uint8_t* q_colT, float* s_col, int64_t P,
+    void* stream) {
+  if (E < 1 || E > kMaxExperts || M < 0 || M > 0x7FFFFFFF || N <= 0 || N % 16 || lddy < N ||
+      P % 128 || P < grouped_padded_rows(M, E) || P > 0x7FFFFFFF || N >= kMaxTmaCoord)
+    return FP8Q_ERR_SHAPE;
+  if (M == 0) return FP8Q_OK;
+  if (!dy || !offsets || !q_colT || !s_col || (q_row != nullptr) != (s_row != nullptr))
+    return FP8Q_ERR_NULL;
+  if (q_row && (lds_row < M || lds_row % 4)) return FP8Q_ERR_SHAPE;
+  if (!aligned16(dy) || !aligned4(offsets) || !aligned16(q_colT) || !aligned16(s_col) || lddy % 8 ||
+      (q_row && (!aligned16(q_row) || !aligned16(s_row))))
+    return FP8Q_ERR_ALIGN;
+  if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
+  CUtensorMap tmd, tmq, tmqt;
+  if (!encode_tmap_2d(&tmd, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, N, M, lddy * 2, 128, 128,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_tmap_2d(&tmqt, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_colT, P, N, P, 128, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+    return FP8Q_ERR_UNSUPPORTED;
+  if (q_row && !encode_tmap_2d(&tmq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_row, N, M, N, 128, 16,
+                               CU_TENSOR_MAP_SWIZZLE_NONE))
+    return FP8Q_ERR_UNSUPPORTED;
+  if (!q_row) tmq = tmqt;  // unused
+  unsigned* err = device_error_word();
+  if (!err) return FP8Q_ERR_CUDA;
+  const int64_t tiles = grouped_padded_rows(M, E) / 128 * ((N + 127) / 128);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t smem = a6_smem<TileGrad>() + group_table_bytes(static_cast<int>(E));
+  const TileGroups grp{offsets, static_cast<int>(E), P, q_row};
+  auto kern = q_row ? a6_tile_kernel<TileGrad, true, true> : a6_tile_kernel<TileGrad, false, true>;
+  static std::atomic<int> smem_ok[2][64];
+  if (!allow_max_smem(kern, smem_ok[q_row ? 1 : 0])) return FP8Q_ERR_CUDA;
+  kern<<<grid_for(tiles, 1), kA6Threads, smem, st>>>(tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row,
+                                                     lds_row, s_col, err, kWaitLimitNs, grp);
+  return launch_status("grouped_transpose_quant_bf16 launch");
+}
+
+extern "C" fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const float* s,
+                                                        const int32_t* offsets, int64_t E,
+                                                        int64_t M, int64_t K, int64_t lds,
+                                                        uint8_t* qT, float* sT, int64_t P,
+                                                        void* stream) {
+  if (E < 1 || E > kMaxExperts || M < 0 || M > 0x7FFFFFFF || K <= 0 || K % 16 || lds < M ||
+      P % 128 || P < grouped_padded_rows(M, E) || P > 0x7FFFFFFF || K >= kMaxTmaCoord)
+    return FP8Q_ERR_SHAPE;
+  if (M == 0) return FP8Q_OK;
+  if (!q || !s || !offsets || !qT || !sT) return FP8Q_ERR_NULL;
+  if (!aligned16(q) || !aligned16(s) || !aligned4(offsets) || !aligned16(qT) || !aligned16(sT) ||
+      lds % 4)
+    return FP8Q_ERR_ALIGN;
+  if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
+  const int64_t KB = (K + 127) / 128;
+  CUtensorMap tmq, tms;
+  if (!encode_tmap_2d(&tmq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, M, K, 128, 128,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_tmap_2d(&tms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, s, M, KB, lds * 4, 132, 1,
+                      CU_TENSOR_MAP_SWIZZLE_NONE))
+    return FP8Q_ERR_UNSUPPORTED;
+  unsigned* err = device_error_word();
+  if (!err) return FP8Q_ERR_CUDA;
+  const int64_t tiles = grouped_padded_rows(M, E) / 128 * KB;
+  const size_t smem = grouped_tile_smem_fp8(static_cast<int>(E));
+  static std::atomic<int> occ[64];
+  const int per_sm = resident_ctas(transpose_quant_fp8_kernel<true>, 256,
+                                   grouped_tile_smem_fp8(kMaxExperts), occ);
+  const TileGroups grp{offsets, static_cast<int>(E), P, nullptr};
+  transpose_quant_fp8_kernel<true><<<grid_for(tiles, per_sm), 256, smem,
+                                     static_cast<cudaStream_t>(stream)>>>(
+      tmq, tms, M, K, qT, sT, err, kWaitLimitNs, grp);
+  return launch_status("grouped_transpose_quant_fp8 launch");
 }

@@ -68,6 +68,8 @@ typedef int fp8q_status;
 #define FP8Q_ERR_CUDA 4        /* the launch failed (cudaGetLastError)               */
 #define FP8Q_ERR_TIMEOUT 5     /* a kernel gave up a bounded wait (device error word) */
 #define FP8Q_ERR_UNSUPPORTED 6 /* no sm_100 device / driver entry point missing     */
+#define FP8Q_ERR_OFFSETS 7     /* a grouped kernel met offsets that decrease or leave
+                                  the rows, and clamped them (device error word)     */
 
 /* Human-readable name of a status code (static storage). */
 const char* fp8q_status_string(fp8q_status status);
@@ -80,7 +82,8 @@ const char* fp8q_last_error_message(void);
 int fp8q_version(void);
 
 /* Synchronises `stream`, then reads the device error word that kernels set when a
- * bounded wait gives up (FP8Q_ERR_TIMEOUT) and, if `clear` != 0, resets it.
+ * bounded wait gives up (FP8Q_ERR_TIMEOUT) or a grouped call's offsets had to be clamped
+ * (FP8Q_ERR_OFFSETS) and, if `clear` != 0, resets it.
  * Returns FP8Q_OK when no kernel reported an error. For tests and diagnostics. */
 fp8q_status fp8q_device_error(void* stream, int clear);
 
@@ -115,6 +118,21 @@ fp8q_status fp8q_quant_weight_128x128(const uint16_t* w, int64_t N, int64_t K, i
 fp8q_status fp8q_rmsnorm_quant(const uint16_t* x, const uint16_t* gamma, int64_t M,
                                int64_t H, int64_t ldx, float eps, uint8_t* q, float* s,
                                int64_t lds, void* stream);
+
+/* a3 with the residual addition in front of it (the pre-norm residual stream of a decoder
+ * layer; "Implementación", fused RMSNorm kernels):
+ *   h = bf16(fl32(x + res)), then the RMSNorm of h and the 1x128 quantization, bit for bit
+ *   fp8q_rmsnorm_quant on h.
+ *   x, res, h [M][H] BF16 (row strides ldx, ldres, ldh), gamma [H] BF16, q [M][H],
+ *   s [G(H)][lds]. h may be x or res itself (same address and stride: the residual stream
+ *   updated in place); any other overlap of h with an input is refused (FP8Q_ERR_SHAPE).
+ * The backward is fp8q_rmsnorm_bwd_quant_dual on h with dres = the gradient of h that
+ * arrives along the residual stream: its `out` is the gradient of both x and res.
+ * Requires H % 16 == 0, H <= 16384. */
+fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t* res,
+                                   const uint16_t* gamma, int64_t M, int64_t H, int64_t ldx,
+                                   int64_t ldres, float eps, uint16_t* h, int64_t ldh,
+                                   uint8_t* q, float* s, int64_t lds, void* stream);
 
 /* a4. SwiGLU fused with 1x128 quantization ("Implementación", fused activation
  * kernels). gu [M][2I] BF16 holds the gate in columns 0..I-1 and the up projection
@@ -310,6 +328,81 @@ fp8q_status fp8q_linear_wgrad_acc_f32(const uint8_t* qdyT, const float* sdy_c,
                                       const uint8_t* qxT, const float* sx_c, int64_t M,
                                       int64_t N, int64_t K, float* dw, int64_t lddw,
                                       void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * The linear layer with one weight per expert (a mixture-of-experts layer in the same
+ * FP8 scheme; the pages train dense models and have no counterpart).
+ *
+ * Token rows are sorted by expert. `offsets` (int32, DEVICE memory, E + 1 entries, 4-byte
+ * aligned) gives expert e the rows offsets[e] .. offsets[e + 1] - 1 of every [M][...]
+ * array; an expert may have no rows, and rows before offsets[0] or from offsets[E] on
+ * belong to nobody: nothing is written for them. M is the rows the arrays hold. The
+ * kernels read the offsets, so a call never waits for the host, and a captured graph can
+ * be replayed with other offsets. 0 <= offsets[0] <= ... <= offsets[E] <= M: entries that
+ * break this are clamped to [0, M] and to the largest entry before them, and reported by
+ * fp8q_device_error as FP8Q_ERR_OFFSETS. 1 <= E <= 1024; M = 0 is allowed (nothing to do;
+ * pointers that hold no elements may then be NULL).
+ *
+ * The experts' weights are quantized by one fp8q_quant_weight_128x128 over the stacked
+ * [E*N][K] matrix (N % 128 == 0, so no block spans two experts): qw [E][N][K],
+ * sw [E][N/128][K/128], and qwT [K][E][N] (its transposed copy, [K][E*N]).
+ *
+ * Column-wise (128x1) groups restart at each expert: expert e has G(rows of e) groups, the
+ * last one filled up with zero codes, and the transposed arrays hold the experts' groups
+ * one after the other: with c_e = G(rows of 0) + ... + G(rows of e - 1), column
+ * 128*c_e + i of qT [..][P] is row offsets[e] + i of expert e, and its groups' scales are
+ * rows c_e .. of sT [P/128][..]. Columns and scale rows past the last group are not
+ * written (and not read). P is the caller's, a multiple of 128, at least
+ * fp8q_grouped_padded_rows(M, E), which is enough whatever the offsets are. */
+
+/* 128 * floor((M + 127 * min(E, M)) / 128), or -1 unless 1 <= E <= 1024, 0 <= M < 2^31. */
+int64_t fp8q_grouped_padded_rows(int64_t M, int64_t E);
+
+/* Forward: y[m,:] = the forward GEMM of row m with its expert's weight; the bits of
+ * fp8q_linear_fwd on that expert's rows alone.
+ *   qa [M][K], sa [K/128][ldsa], qw [E][N][K], sw [E][N/128][K/128], y [M][N] BF16 (ldy).
+ * Requires N % 128 == 0, K % 128 == 0, E*N < 2^31. */
+fp8q_status fp8q_grouped_linear_fwd(const uint8_t* qa, const float* sa, int64_t ldsa,
+                                    const uint8_t* qw, const float* sw, const int32_t* offsets,
+                                    int64_t E, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                                    int64_t ldy, void* stream);
+
+/* DGrad: dx[m,:] = fp8q_linear_dgrad of row m with its expert's weight, bit for bit.
+ *   qdy [M][N], sdy [N/128][ldsdy], qwT [K][E][N], sw [E][N/128][K/128],
+ *   dx [M][K] BF16 (lddx). Requires N % 128 == 0, K % 128 == 0, E*N < 2^31. */
+fp8q_status fp8q_grouped_linear_dgrad(const uint8_t* qdy, const float* sdy, int64_t ldsdy,
+                                      const uint8_t* qwT, const float* sw,
+                                      const int32_t* offsets, int64_t E, int64_t M, int64_t N,
+                                      int64_t K, uint16_t* dx, int64_t lddx, void* stream);
+
+/* The BF16 gradient quantized for both backward products: row-wise 1x128 for DGrad
+ * (q_row [M][N], s_row [G(N)][lds_row]; may be NULL) and column-wise 128x1 per expert for
+ * WGrad (q_colT [N][P], s_col [P/128][N]).
+ *   dy [M][N] BF16, row stride lddy. Requires N % 16 == 0. */
+fp8q_status fp8q_grouped_transpose_quant_bf16(const uint16_t* dy, const int32_t* offsets,
+                                              int64_t E, int64_t M, int64_t N, int64_t lddy,
+                                              uint8_t* q_row, float* s_row, int64_t lds_row,
+                                              uint8_t* q_colT, float* s_col, int64_t P,
+                                              void* stream);
+
+/* The saved FP8 activation (1x128 groups) re-grouped 128x1 per expert for WGrad:
+ * xhat = fl32(s * dec(q)), as fp8q_transpose_quant_fp8.
+ *   q [M][K], s [G(K)][lds] -> qT [K][P], sT [P/128][K]. Requires K % 16 == 0. */
+fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const float* s,
+                                             const int32_t* offsets, int64_t E, int64_t M,
+                                             int64_t K, int64_t lds, uint8_t* qT, float* sT,
+                                             int64_t P, void* stream);
+
+/* WGrad: dw[e] = fp8q_linear_wgrad over expert e's groups, bit for bit; zeros for an
+ * expert without rows.
+ *   qdyT [N][P], sdy_c [P/128][N], qxT [K][P], sx_c [P/128][K] (the same P for both),
+ *   dw [E][N][K] BF16 (row stride lddw, experts N * lddw apart).
+ * Requires N % 128 == 0, K % 128 == 0, P % 128 == 0, E*N < 2^31. Groups that reach past
+ * P are dropped and reported as FP8Q_ERR_OFFSETS. */
+fp8q_status fp8q_grouped_linear_wgrad(const uint8_t* qdyT, const float* sdy_c,
+                                      const uint8_t* qxT, const float* sx_c,
+                                      const int32_t* offsets, int64_t E, int64_t P, int64_t N,
+                                      int64_t K, uint16_t* dw, int64_t lddw, void* stream);
 
 /* Diagnostic: launches one CTA that waits on a barrier nothing completes, with a
  * wait limit of `limit_ns` nanoseconds, exactly as the GEMM's bounded waits do.
