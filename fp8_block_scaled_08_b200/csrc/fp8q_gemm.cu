@@ -819,27 +819,7 @@ fp8q_status launch_gemm(const uint8_t* A, const uint8_t* B, int64_t Mg, int64_t 
   return launch_status("gemm_kernel launch");
 }
 
-// The products of a grouped call on the pair kernel. Forward / DGrad (kCol false):
-// A [rows][Kg] and out [rows][Ng] hold the experts' rows one after the other, B is one
-// tensor map over all experts' weights (b_inner x b_outer bytes) in which expert e starts
-// at (e * bx_step, e * by_step), its block scales at sb + e * sb_se. WGrad (kCol true):
-// A [Mg][P] and B [Ng][P] hold the experts' 128-row groups one after the other along P,
-// out [E * Mg][Ng] the experts' products.
-struct GroupedGemm {
-  const uint8_t *A, *B;
-  int64_t rows;  // token rows (forward, DGrad) / P (WGrad)
-  int64_t E, Mg, Ng, Kg;
-  int64_t b_inner, b_outer, bx_step, by_step;
-  const float* sa;
-  int64_t ldsa;
-  const float* sb;
-  int64_t sb_sj, sb_sr, sb_se;
-  const float* sbcol;
-  const int32_t* offsets;
-  void* y;
-  int64_t ldy;
-};
-
+// The products of a grouped call (GroupedGemm) on the pair kernel.
 template <bool kCol>
 fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
   if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
@@ -899,6 +879,13 @@ fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
   gemm_kernel<kCol, false, true>
       <<<grid, kThreads, kGroupedSmemBytes, stream>>>(tmA, tmB, tmSA, tmSB, tmY, p);
   return launch_status("grouped gemm_kernel launch");
+}
+
+// Forward or DGrad: up to kStripMaxRows rows per expert on average (of the rows the arrays
+// hold; the routing itself is known on the device only) take the strip kernel.
+fp8q_status launch_grouped_rows(const GroupedGemm& g, cudaStream_t stream) {
+  if (g.out_extents_ok() && g.rows <= kStripMaxRows * g.E) return launch_grouped_strips(g, stream);
+  return launch_grouped<false>(g, stream);
 }
 
 }  // namespace
@@ -996,7 +983,7 @@ extern "C" fp8q_status fp8q_grouped_linear_fwd(const uint8_t* qa, const float* s
   const int64_t NB = N / 128, KB = K / 128;
   const GroupedGemm g = {qa, qw, M,  E,  M,  N,       K,       K,       E * N,  0,
                          N,  sa, ldsa, sw, KB, 1, NB * KB, nullptr, offsets, y, ldy};
-  return launch_grouped<false>(g, static_cast<cudaStream_t>(stream));
+  return launch_grouped_rows(g, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8q_status fp8q_grouped_linear_dgrad(const uint8_t* qdy, const float* sdy,
@@ -1018,7 +1005,7 @@ extern "C" fp8q_status fp8q_grouped_linear_dgrad(const uint8_t* qdy, const float
   const int64_t NB = N / 128, KB = K / 128;
   const GroupedGemm g = {qdy, qwT, M,   E,     M,  K, N,  E * N,   K,       N, 0,
                          sdy, ldsdy, sw, 1, KB, NB * KB, nullptr, offsets, dx, lddx};
-  return launch_grouped<false>(g, static_cast<cudaStream_t>(stream));
+  return launch_grouped_rows(g, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8q_status fp8q_grouped_linear_wgrad(const uint8_t* qdyT, const float* sdy_c,

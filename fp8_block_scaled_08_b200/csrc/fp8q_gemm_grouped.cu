@@ -1,0 +1,449 @@
+// Grouped block-scaled FP8 products for few rows per expert (decoding, small ragged
+// batches), sm_100a: the forward and DGrad of a layer with one weight per expert,
+//
+//   out[i, j] = sum_r  sA(i, r) * sB(e, j / 128, r) * sum_{l in slice r} qA[i, l] * qB_e[j, l]
+//
+// for the rows i of expert e, with the arithmetic of the large-tile kernel (each 128-wide
+// slice an FP8 tensor-core product in fp32, acc = fma(P_r, sA * sB, acc) in increasing r
+// from +0), so that a row has the same bits whichever kernel the sizes select.
+//
+// With a few rows per expert the product is bound by reading every active expert's FP8
+// weights once (2 flops per weight byte and row, far below the tensor cores' rate), so:
+//
+//  * The weights are the MMA's M side: a tile is 128 weight rows x at most kNT token rows,
+//    so an expert with few tokens costs an MMA of N = kNT (32 .. 128) and the token rows
+//    ride along, instead of 128 or 256 mostly empty token rows per MMA.
+//  * Persistent CTAs, one per SM, walk the tiles of all experts that have rows (expert by
+//    expert, the token tiles of a strip next to each other so that they share its weights
+//    in L2); the copies of the next tile start while this one is multiplied, promoted and
+//    stored, so the weight stream does not stop between tiles or experts.
+//  * A ring of stages of kG consecutive slices, up to 200 KB in all: one 3D tensor copy
+//    brings kG * 128 bytes of each of the weight rows, another the token rows of the same
+//    slices (single-slice stages measured 1-4 % slower: twice the copies and barriers).
+//  * Warp 0 is the producer; warps 1 and 2 issue the MMAs of alternate stages into up to 8
+//    TMEM buffers of kG slices; the other warps promote a buffer at a time (figures at
+//    launch_grouped_strips): lane l of warp w holds weight row 32 * (w % 4) + l and the
+//    accumulators of the tile's tokens (of half of them, in two warpgroups, from 64 tokens
+//    on; four warpgroups measured up to 19 % slower); a slice's token scales are read from
+//    shared memory as broadcasts and multiplied by the block scale.
+//  * Epilogue: two lanes exchange halves so that each stores two neighbouring outputs of
+//    one token (a warp store writes two runs of 64 bytes).
+//
+// The first token row of an expert's tiles is rounded down to a multiple of 4 (the row
+// scales come by tensor copy, whose innermost coordinate is a multiple of 16 bytes); rows
+// of other experts in a tile are multiplied and not stored.
+// Every mbarrier wait is bounded; a wait that gives up records FP8Q_ERR_TIMEOUT in the
+// device error word and the CTA winds down.
+#include <algorithm>
+#include <atomic>
+
+#include "fp8q_device.cuh"
+#include "fp8q_grouped.cuh"
+#include "fp8q_host.h"
+
+namespace fp8q {
+namespace {
+
+constexpr int kGmIssuers = 2;    // warps 1 and 2
+constexpr int kGmPromote = 3;    // first promotion warp
+constexpr int kGmRows = 128;     // weight rows of a tile
+constexpr int kGmBK = 128;
+constexpr int kGmMaxStages = 8;
+constexpr int kGmScRing = 8;     // row-scale slots (one per stage's slices)
+constexpr uint32_t kGmMaxSmem = 232448;
+
+template <int kNT>
+struct GmShape {
+  static constexpr int kG = 2;  // slices per stage, accumulator buffer and row-scale slot
+  static constexpr int kBufs = kNT * kG <= 64 ? 8 : 512 / (kNT * kG);  // accumulator buffers
+  static constexpr uint32_t kTmemCols = kBufs * kG * kNT;
+  static constexpr int kHalves = kNT >= 64 ? 2 : 1;        // promotion warpgroups
+  static constexpr int kCols = kNT / kHalves;              // token columns of each
+  static constexpr int kThreads = 32 * (kGmPromote + 4 * kHalves);
+  static constexpr uint32_t kWBytes = kG * kGmRows * kGmBK;
+  static constexpr uint32_t kXBytes = kG * kNT * kGmBK;
+  static constexpr uint32_t kStage = kWBytes + kXBytes;
+  static constexpr uint32_t kSlot = kG * kNT * 4;  // a multiple of 128
+  static constexpr uint32_t kBars = 2 * kGmMaxStages + 2 * kBufs + 2 * kGmScRing + 1;
+  static constexpr uint32_t kFixed = kGmScRing * kSlot + kBars * 8 + 16;
+  static_assert(kBufs % kGmIssuers == 0, "an accumulator buffer is always the same issuer's");
+  static_assert(kNT % 16 == 0 && kNT <= 256 && kSlot % 128 == 0, "MMA N and copy alignment");
+  static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512,
+                "TMEM allocations are powers of two");
+};
+
+struct GmParams {
+  const int32_t* offsets;
+  int32_t experts, rows;
+  int32_t strips;    // strips of one expert's weight
+  int32_t kblocks;   // slices of the reduction
+  int32_t stages;
+  int32_t height;    // weight rows of a strip: 128, 64 or 32
+  int32_t wy_step;   // an expert's step in the weight map: rows
+  int32_t wz_step;   // and slices
+  const float* sb;   // block scale of (e, strip, slice): sb[e*sb_se + strip*sb_sj + slice*sb_sr]
+  int64_t sb_se, sb_sj, sb_sr;
+  uint16_t* y;
+  int64_t ldy;
+  unsigned* err;
+  uint64_t wait_limit_ns;
+};
+
+struct GmTile {
+  int e, strip, row0, lo, hi;
+};
+
+template <int kNT>
+__device__ __forceinline__ int gm_token_tiles(int lo, int hi) {
+  return hi > lo ? (hi - (lo & ~3) + kNT - 1) / kNT : 0;
+}
+
+template <int kNT>
+__device__ __forceinline__ GmTile gm_tile(int t, const GmParams& p, const int* off,
+                                          const int* first) {
+  GmTile g;
+  g.e = group_find(first, p.experts, t / p.strips);
+  const int tt = first[g.e + 1] - first[g.e];
+  const int w = t - first[g.e] * p.strips;
+  g.strip = w / tt;
+  g.lo = off[g.e];
+  g.hi = off[g.e + 1];
+  g.row0 = (g.lo & ~3) + (w - g.strip * tt) * kNT;
+  return g;
+}
+
+__device__ __forceinline__ void gm_wait_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) return;
+  }
+}
+
+// 16 or 32 accumulator columns of this warp's lane quarter.
+template <int kC>
+__device__ __forceinline__ void gm_tmem_load(uint32_t taddr, uint32_t (&r)[kC]) {
+  static_assert(kC == 16 || kC == 32, "tcgen05.ld widths");
+  if constexpr (kC == 16) tmem_ld16(taddr, r);
+  else tmem_ld32(taddr, r);
+}
+
+template <int kNT>
+__global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kernel(
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+    const __grid_constant__ CUtensorMap tmSA, const GmParams p) {
+  using S = GmShape<kNT>;
+  constexpr int kBufs = S::kBufs, kG = S::kG;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int stages = p.stages;
+  uint8_t* slots = smem + static_cast<uint32_t>(stages) * S::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(slots + kGmScRing * S::kSlot);
+  uint64_t* empty = full + kGmMaxStages;
+  uint64_t* tfull = empty + kGmMaxStages;
+  uint64_t* tempty = tfull + kBufs;
+  uint64_t* sfull = tempty + kBufs;
+  uint64_t* sempty = sfull + kGmScRing;
+  uint64_t* done = sempty + kGmScRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* off = reinterpret_cast<int*>(tmem_slot + 4);
+  int* first = off + p.experts + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, kGmIssuers);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(tfull + b, 1);
+      mbar_init(tempty + b, (p.height >> 5) * S::kHalves);
+    }
+    for (int i = 0; i < kGmScRing; ++i) {
+      mbar_init(sfull + i, 1);
+      mbar_init(sempty + i, (p.height >> 5) * S::kHalves);
+    }
+    mbar_init(done, kGmIssuers);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmSA);
+  }
+  group_table_fill(off, first, p.offsets, p.experts, p.rows, p.err, gm_token_tiles<kNT>);
+  if (warp == 1) tmem_alloc<S::kTmemCols>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.err, p.wait_limit_ns};
+  const int num_tiles = first[p.experts] * p.strips;
+  const int KB = p.kblocks;
+  const int nst = (KB + kG - 1) / kG;  // accumulator buffers of a tile
+  const int quarters = p.height >> 5;  // TMEM lane quarters that hold weight rows
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int s = 0, si = 0;
+      uint32_t ph = 0, sph = 0;
+      uint32_t issued = 0, par = 0, sc_issued = 0, sc_par = 0;  // as in the large-tile kernel
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+        const GmTile g = gm_tile<kNT>(t, p, off, first);
+        const int wy = g.e * p.wy_step + g.strip * p.height, wz = g.e * p.wz_step;
+        for (int kb = 0; kb < KB; kb += kG) {
+          if (!mbar_wait(empty + s, ph ^ 1u, ctl)) { ok = false; break; }
+          mbar_arrive_expect_tx(full + s, kG * kGmBK * p.height + S::kXBytes);
+          tma_load_3d(smem + s * S::kStage, &tmW, 0, wy, wz + kb, full + s);
+          tma_load_3d(smem + s * S::kStage + S::kWBytes, &tmX, 0, g.row0, kb, full + s);
+          issued |= 1u << s;
+          par = (par & ~(1u << s)) | (ph << s);
+          if (++s == stages) { s = 0; ph ^= 1u; }
+          if (!mbar_wait(sempty + si, sph ^ 1u, ctl)) { ok = false; break; }
+          mbar_arrive_expect_tx(sfull + si, S::kSlot);
+          tma_load_2d(slots + si * S::kSlot, &tmSA, g.row0, kb, sfull + si);
+          sc_issued |= 1u << si;
+          sc_par = (sc_par & ~(1u << si)) | (sph << si);
+          if (++si == kGmScRing) { si = 0; sph ^= 1u; }
+        }
+      }
+      if (!ok) {  // let the copies still in flight land before the CTA exits
+        for (int i = 0; i < stages; ++i)
+          if ((issued >> i) & 1u) gm_wait_drain(full + i, (par >> i) & 1u, p.wait_limit_ns);
+        for (int i = 0; i < kGmScRing; ++i)
+          if ((sc_issued >> i) & 1u) gm_wait_drain(sfull + i, (sc_par >> i) & 1u, p.wait_limit_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp <= kGmIssuers) {
+    // ------------------------------------------------------------ MMA issuers
+    if (lane == 0) {
+      // Issuer i takes the accumulator buffers i, i + 2, ... of this CTA: kG slices of kNT
+      // columns each, then one commit for the buffer. Both issuers follow every stage (the
+      // other one's they hand back at once): an issuer that met a stage only every second
+      // time it is filled could not tell those two phases apart by their parity.
+      const uint32_t issuer = static_cast<uint32_t>(warp - 1);
+      const uint32_t idesc = idesc_e4m3_f32(kGmRows, kNT);
+      int s = 0;
+      uint32_t ph = 0, it = 0;  // it: accumulator buffers filled by this CTA so far
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+        for (int kb = 0; ok && kb < KB; kb += kG, ++it) {
+          const bool mine = it % kGmIssuers == issuer;
+          const uint32_t buf = it % kBufs, tph = (it / kBufs) & 1u;
+          if (mine && !mbar_wait(tempty + buf, tph ^ 1u, ctl)) { ok = false; break; }
+          if (!mbar_wait(full + s, ph, ctl)) { ok = false; break; }
+          if (mine) {
+            tc_fence_after();
+            const uint32_t w0 = smem_u32(smem + s * S::kStage);
+            const uint32_t x0 = w0 + S::kWBytes;
+#pragma unroll
+            for (int j = 0; j < kG; ++j)
+              if (kb + j < KB)
+                mma_f8f6f4_slice(tmem_base + (buf * kG + j) * kNT,
+                                 smem_desc_k_sw128(w0 + j * p.height * kGmBK),
+                                 smem_desc_k_sw128(x0 + j * kNT * kGmBK), idesc);
+            mma_commit(tfull + buf);
+            mma_commit(empty + s);
+          } else {
+            mbar_arrive(empty + s);
+          }
+          if (++s == stages) { s = 0; ph ^= 1u; }
+        }
+      }
+      mma_commit(done);
+      gm_wait_drain(done, 0, p.wait_limit_ns);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ promotion + epilogue
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    const int my_tiles = q < quarters ? num_tiles : 0;  // a low strip leaves quarters idle
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    // columns loaded at a time: 32 per slice, 16 where 64 accumulators leave no room
+    constexpr int kCols = S::kCols, kChunk = kCols == 32 ? 32 : 16;
+    const int col0 = ((warp - kGmPromote) >> 2) * kCols;  // this warpgroup's tokens
+    uint32_t it = 0, si = 0, sph = 0;
+    bool ok = true;
+    // block scales, 32 slices at a time: lane l holds slice 32 * (kb / 32) + l
+    auto sb_fetch = [&](const GmTile& g, int kk) -> float {
+      return kk < KB ? __ldg(p.sb + g.e * p.sb_se + ((g.strip * p.height) >> 7) * p.sb_sj +
+                                kk * p.sb_sr) : 0.0f;
+    };
+    GmTile g{};
+    float sbv = 0.0f;
+    if (static_cast<int>(blockIdx.x) < my_tiles) {
+      g = gm_tile<kNT>(blockIdx.x, p, off, first);
+      sbv = sb_fetch(g, lane);
+    }
+    for (int t = blockIdx.x; ok && t < my_tiles; t += gridDim.x) {
+      float acc[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+      float sbx = 0.0f;
+      for (int k = 0; k < nst; ++k) {
+        const int kb = k * kG;
+        if ((kb & 31) == 16) sbx = sb_fetch(g, kb + 16 + lane);
+        if ((kb & 31) == 0 && kb > 0) sbv = sbx;
+        float sb[kG];
+#pragma unroll
+        for (int j = 0; j < kG; ++j) sb[j] = __shfl_sync(0xFFFFFFFFu, sbv, (kb + j) & 31);
+        if (!mbar_wait_warp(sfull + si, sph, ctl)) { ok = false; break; }
+        const float4* sa = reinterpret_cast<const float4*>(slots + si * S::kSlot) + col0 / 4;
+        const uint32_t buf = it % kBufs, tph = (it / kBufs) & 1u;
+        if (!mbar_wait_warp(tfull + buf, tph, ctl)) { ok = false; break; }
+        tc_fence_after();
+        const bool whole = kb + kG <= KB;  // a last stage may hold fewer slices
+#pragma unroll
+        for (int c = 0; c < kCols; c += kChunk) {
+          // the loads of all slices of the buffer are in flight together
+          uint32_t r[kG][kChunk];
+#pragma unroll
+          for (int j = 0; j < kG; ++j)
+            gm_tmem_load<kChunk>(lane_base + (buf * kG + j) * kNT + col0 + c, r[j]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < kG; ++j) {
+            if (j == 0 || whole) {
+#pragma unroll
+              for (int i = 0; i < kChunk; i += 4) {
+                const float4 s4 = sa[(j * kNT + c + i) / 4];  // broadcast
+                float s0, s1, s2, s3;
+                mul2(s0, s1, s4.x, s4.y, sb[j], sb[j]);
+                mul2(s2, s3, s4.z, s4.w, sb[j], sb[j]);
+                float* a = acc + c + i;
+                fma2(a[0], a[1], __uint_as_float(r[j][i]), __uint_as_float(r[j][i + 1]), s0, s1);
+                fma2(a[2], a[3], __uint_as_float(r[j][i + 2]), __uint_as_float(r[j][i + 3]), s2, s3);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(tempty + buf);
+          mbar_arrive(sempty + si);
+        }
+        ++it;
+        if (++si == kGmScRing) { si = 0; sph ^= 1u; }
+      }
+      if (!ok) break;
+      const GmTile o = g;
+      if (t + static_cast<int>(gridDim.x) < my_tiles) {  // the next tile's scales meanwhile
+        g = gm_tile<kNT>(t + gridDim.x, p, off, first);
+        sbv = sb_fetch(g, lane);
+      }
+      // lanes 2i and 2i + 1 exchange: the even lane stores both outputs of token j, the odd
+      // lane those of token j + 1
+      const int odd = lane & 1;
+      uint16_t* dst = p.y + static_cast<int64_t>(o.row0 + col0 + odd) * p.ldy + o.strip * p.height +
+                      q * 32 + lane - odd;
+      const int lo = o.lo - o.row0 - col0 - odd, hi = o.hi - o.row0 - col0 - odd;
+#pragma unroll
+      for (int j = 0; j < kCols; j += 2) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[j] : acc[j + 1], 1);
+        const uint32_t v = odd ? pack_bf16x2(other, acc[j + 1]) : pack_bf16x2(acc[j], other);
+        if (j >= lo && j < hi) *reinterpret_cast<uint32_t*>(dst + j * p.ldy) = v;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<S::kTmemCols>(tmem_base);
+  }
+}
+
+template <int kNT>
+fp8q_status launch_strips(const GroupedGemm& g, int sms, cudaStream_t stream) {
+  using S = GmShape<kNT>;
+  const int64_t KB = g.Kg / kGmBK;
+  const uint32_t fixed = 1024 + S::kFixed + group_table_bytes(static_cast<int>(g.E));
+  GmParams p = {};
+  p.stages = static_cast<int32_t>(
+      std::min<uint32_t>(kGmMaxStages, (kGmMaxSmem - fixed) / S::kStage));
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * S::kStage;
+  // Strip height: 128 rows fill the MMA; where even one tile for every expert that can have
+  // rows leaves half of the SMs without one, lower strips (the rest of the MMA's rows is
+  // whatever the stage holds, its lanes are never read) put more SMs on the weights.
+  p.height = kGmRows;
+  while (p.height > 32 && std::min(g.E, g.rows) * (g.Ng / p.height) * 2 <= sms) p.height /= 2;
+  CUtensorMap tmW, tmX, tmSA;
+  const uint64_t wdims[3] = {kGmBK, static_cast<uint64_t>(g.b_outer),
+                             static_cast<uint64_t>(g.b_inner / kGmBK)};
+  const uint64_t wstr[2] = {static_cast<uint64_t>(g.b_inner), kGmBK};
+  const uint32_t wbox[3] = {kGmBK, static_cast<uint32_t>(p.height), S::kG};
+  const uint64_t xdims[3] = {kGmBK, static_cast<uint64_t>(g.rows), static_cast<uint64_t>(KB)};
+  const uint64_t xstr[2] = {static_cast<uint64_t>(g.Kg), kGmBK};
+  const uint32_t xbox[3] = {kGmBK, kNT, S::kG};
+  if (!encode_tmap_3d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.B, wdims, wstr, wbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_3d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.A, xdims, xstr, xbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_2d(&tmSA, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.sa, g.rows, KB, g.ldsa * 4, kNT,
+                      S::kG, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return FP8Q_ERR_UNSUPPORTED;
+  p.offsets = g.offsets;
+  p.experts = static_cast<int32_t>(g.E);
+  p.rows = static_cast<int32_t>(g.rows);
+  p.strips = static_cast<int32_t>(g.Ng / p.height);
+  p.kblocks = static_cast<int32_t>(KB);
+  p.wy_step = static_cast<int32_t>(g.by_step);
+  p.wz_step = static_cast<int32_t>(g.bx_step / kGmBK);
+  p.sb = g.sb;
+  p.sb_se = g.sb_se;
+  p.sb_sj = g.sb_sj;
+  p.sb_sr = g.sb_sr;
+  p.y = static_cast<uint16_t*>(g.y);
+  p.ldy = g.ldy;
+  p.err = device_error_word();
+  p.wait_limit_ns = kWaitLimitNs;
+  if (!p.err) return FP8Q_ERR_CUDA;
+  // token tiles at most: each expert with rows adds a partial tile and up to 3 rows
+  const int64_t tiles = (g.rows + (kNT + 2) * std::min(g.E, g.rows)) / kNT * p.strips;
+  if (tiles > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
+  static std::atomic<int> smem_ok[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
+  if (!smem_ok[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(grouped_strip_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kGmMaxSmem));
+    if (e != cudaSuccess) {
+      set_last_error("cudaFuncSetAttribute(grouped strips)", e);
+      cudaGetLastError();
+      return FP8Q_ERR_CUDA;
+    }
+    smem_ok[dev].store(1, std::memory_order_release);
+  }
+  grouped_strip_kernel<kNT><<<static_cast<int>(std::min<int64_t>(tiles, sms)), S::kThreads, smem,
+                              stream>>>(tmW, tmX, tmSA, p);
+  return launch_status("grouped_strip_kernel launch");
+}
+
+}  // namespace
+
+fp8q_status launch_grouped_strips(const GroupedGemm& g, cudaStream_t stream) {
+  const int sms = sm100_sm_count();
+  if (!sms) return FP8Q_ERR_UNSUPPORTED;
+  // Token rows of a tile, by the average rows of an expert. Measured, one B200, L2 flushed
+  // (us; in brackets the large-tile kernel): forward, 64 experts of 4096 x 4096, at 8 / 16 /
+  // 32 / 64 / 128 rows: 32-row tiles 184 / 184 / 205 / 320 / 562, 64-row tiles 182 / 182 /
+  // 192 / 234 / 375, 128-row tiles 246 / 248 / 250 / 252 / 377 (277 / 281 / 289 / 297 /
+  // 297); DGrad, 16 experts of 3584 x 1024, at 16 / 32 / 64 / 128 rows: 22.6 / 28.7 / 32.8 /
+  // 41.0, 22.6 / 22.6 / 30.7 / 36.9, 24.6 / 26.6 / 26.6 / 41.0 (28.7 / 30.7 / 30.7 / 30.7);
+  // forward, one expert of 4096 x 4096, 1 row: 16.4 with 32-row tiles, 20.5 with 64-row ones.
+  // 184 us are 5.9 TB/s of weights, 0.91 of the measured copy rate. Promoting one slice per
+  // TMEM buffer instead of two took 198 / 239 us at 16 / 32 rows (32- / 64-row tiles).
+  if (g.rows <= 16 * g.E) return launch_strips<32>(g, sms, stream);
+  if (g.rows <= 48 * g.E) return launch_strips<64>(g, sms, stream);
+  return launch_strips<128>(g, sms, stream);
+}
+
+}  // namespace fp8q

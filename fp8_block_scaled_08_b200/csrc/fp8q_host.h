@@ -66,4 +66,36 @@ fp8q_status launch_skinny_gemm(const uint8_t* A, const uint8_t* B, int64_t Mg, i
                                int64_t sb_sj, int64_t sb_sr, uint16_t* y, int64_t ldy,
                                cudaStream_t stream);
 
+// The products of a grouped call. Forward / DGrad:
+// A [rows][Kg] and out [rows][Ng] hold the experts' rows one after the other, B is one
+// tensor map over all experts' weights (b_inner x b_outer bytes) in which expert e starts
+// at (e * bx_step, e * by_step), its block scales at sb + e * sb_se. WGrad:
+// A [Mg][P] and B [Ng][P] hold the experts' 128-row groups one after the other along P,
+// out [E * Mg][Ng] the experts' products.
+struct GroupedGemm {
+  const uint8_t *A, *B;
+  int64_t rows;  // token rows (forward, DGrad) / P (WGrad)
+  int64_t E, Mg, Ng, Kg;
+  int64_t b_inner, b_outer, bx_step, by_step;
+  const float* sa;
+  int64_t ldsa;
+  const float* sb;
+  int64_t sb_sj, sb_sr, sb_se;
+  const float* sbcol;
+  const int32_t* offsets;
+  void* y;
+  int64_t ldy;
+  // every extent is a tensor-copy coordinate
+  bool out_extents_ok() const {
+    return rows <= 0x7FFFFFFF && b_inner <= 0x7FFFFFFF && b_outer <= 0x7FFFFFFF && Kg <= 0x7FFFFFFF;
+  }
+};
+
+// Average rows per expert up to which the forward and DGrad run as strips of weight rows
+// (at 64 rows 252 against 297 us on the large-tile kernel, at 128 rows 375 against 297: see
+// launch_grouped_strips).
+constexpr int64_t kStripMaxRows = 96;
+
+fp8q_status launch_grouped_strips(const GroupedGemm& g, cudaStream_t stream);
+
 }  // namespace fp8q

@@ -138,6 +138,38 @@ def test_wgrad(fq, oracle_mod, name, N, K):
         g += n
 
 
+@pytest.mark.parametrize("counts", [[1, 0, 9, 33, 2, 0, 0, 5], [30, 64, 1, 0, 67, 20, 31, 40],
+                                    [128, 40, 129, 0, 100, 61, 90, 96]])
+@pytest.mark.parametrize("N,K", [(640, 4224), (1280, 128), (2560, 384), (128, 8448)])
+def test_products_over_strip_shapes(fq, counts, N, K):
+    """Few rows per expert: every token-tile width, strip height and odd or long reduction,
+    bit for bit the dense products."""
+    E = len(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    M = int(off[-1])
+    o = dev_offsets(off)
+    qw, sw, qwT = weights(fq, E, N, K, 3045)
+    x = workloads.activations_bf16((M, K), 0, 3046, DEV)
+    dy = workloads.gradients_bf16((M, N), 1e-3, 0, 3047, DEV)
+    qa, sa = fq.quant_act_1x128_alloc(x)
+    q, s = fq.quant_act_1x128_alloc(dy)
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
+    dx = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_fwd(qa, sa, qw, sw, o, y)
+    fq.grouped_linear_dgrad(q, s, qwT, sw, o, dx)
+    torch.cuda.synchronize()
+    assert fq.device_error() == fq.FP8Q_OK
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        qe, se = fq.quant_act_1x128_alloc(x[lo:hi].contiguous())
+        assert same_bits(y[lo:hi], fq.linear_fwd_alloc(qe, se, qw[e], sw[e].clone())), e
+        qe, se = fq.quant_act_1x128_alloc(dy[lo:hi].contiguous())
+        assert same_bits(dx[lo:hi], fq.linear_dgrad_alloc(qe, se, qwT[:, e].contiguous(),
+                                                          sw[e].clone())), e
+
+
 def test_strided_outputs_and_wide_scales(fq):
     """Row strides of y and dx, and scale arrays longer than the rows."""
     off, M, E = route("ragged")
