@@ -554,41 +554,74 @@ def linear_wgrad_acc_f32(qdyT, sdy_c, qxT, sx_c, dw, stream=None):
 # One weight per expert (ragged row groups), and the norm in front of it
 # --------------------------------------------------------------------------
 
-def _row_stride(t, name):
-    """Row stride of a matrix with dense rows (a single row has none: its length)."""
-    if t.stride(-1) != 1 and t.shape[1] > 1:
+def _row_stride(t, rows, cols, name):
+    """Row stride of a [rows, cols] matrix with dense rows (a single row has none: its
+    length)."""
+    r, c = t.stride()
+    if c != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
-    return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
+    return r if rows > 1 else cols
 
 
 def _run(fn, where, stream, ref, *args):
     """Call `fn` on the device of `ref` (the current one or not), on `stream` or that
     device's current stream."""
-    if ref.device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
+    dev = ref.get_device()
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream), where)
     else:
-        with torch.cuda.device(ref.device):
-            _check(fn(*args, _stream(stream)), where)
+        with torch.cuda.device(dev):
+            _check(fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream), where)
 
 
-def _together(*named):
-    """Every operand lies on the first one's device."""
-    dev = named[0][0].device
-    for t, n in named[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError("%s must be on %s, got %s" % (n, dev, t.device))
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _offsets(offsets, experts=None):
+# The same without building a Stream object (3 us of a small call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _pointers(*named):
+    """Device pointers of the operands (0 for None), which all lie on the first one's
+    device."""
+    dev = named[0][0].get_device()
+    if dev < 0:
+        raise ValueError("libfp8q takes CUDA tensors (device pointers)")
+    out = []
+    for t, n in named:
+        if t is None:
+            out.append(None)
+        elif t.get_device() == dev:
+            out.append(t.data_ptr())
+        else:
+            raise ValueError("%s must be on cuda:%d, got %s" % (n, dev, t.device))
+    return out
+
+
+def _exact(t, shape, dtype, name):
+    """_shape for a tuple of ints, with the failing case left to it."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
+        _shape(t, shape, dtype, name)
+
+
+def _exact_dense(t, shape, dtype, name):
+    _exact(t, shape, dtype, name)
+    if not t.is_contiguous():
+        _dense(t, name)
+
+
+def _offsets(offsets):
     """int32 [E + 1]; returns E."""
     if not isinstance(offsets, torch.Tensor):
         raise TypeError("offsets must be a torch.Tensor")
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or (
-            experts is not None and offsets.numel() != experts + 1):
-        raise ValueError("offsets must be an int32 tensor [%s], got %s %s" % (
-            "E + 1" if experts is None else experts + 1, tuple(offsets.shape), offsets.dtype))
-    _dense(offsets, "offsets")
-    return offsets.numel() - 1
+    n = offsets.numel()
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or n < 2:
+        raise ValueError("offsets must be an int32 tensor [E + 1], got %s %s" % (
+            tuple(offsets.shape), offsets.dtype))
+    if not offsets.is_contiguous():
+        _dense(offsets, "offsets")
+    return n - 1
 
 
 def grouped_padded_rows(M, E) -> int:
@@ -605,18 +638,17 @@ def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
     RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]. Its backward is
     rmsnorm_bwd_quant_dual on h."""
     _want(x, torch.bfloat16, 2, "x")
-    _want(gamma, torch.bfloat16, 1, "gamma")
-    _dense(gamma, "gamma"); _dense(q, "q"); _dense(s, "s")
-    M, H = x.shape
-    _shape(res, (M, H), torch.bfloat16, "res")
-    _shape(h, (M, H), torch.bfloat16, "h")
-    _shape(gamma, (H,), torch.bfloat16, "gamma")
-    _shape(q, (M, H), torch.uint8, "q")
-    _scales_1x128(s, _groups(H), M, "s")
-    _together((x, "x"), (res, "res"), (gamma, "gamma"), (h, "h"), (q, "q"), (s, "s"))
-    _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, x, _ptr(x), _ptr(res),
-         _ptr(gamma), M, H, _row_stride(x, "x"), _row_stride(res, "res"), float(eps), _ptr(h),
-         _row_stride(h, "h"), _ptr(q), _ptr(s), s.shape[1])
+    M, H = shape = x.shape
+    _exact(res, shape, torch.bfloat16, "res")
+    _exact(h, shape, torch.bfloat16, "h")
+    _exact_dense(gamma, (H,), torch.bfloat16, "gamma")
+    _exact_dense(q, shape, torch.uint8, "q")
+    _scales_1x128(s, _groups(H), M, "s"); _dense(s, "s")
+    px, pr, pg, ph, pq, ps = _pointers((x, "x"), (res, "res"), (gamma, "gamma"), (h, "h"),
+                                       (q, "q"), (s, "s"))
+    _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, x, px, pr, pg, M, H,
+         _row_stride(x, M, H, "x"), _row_stride(res, M, H, "res"), eps, ph, _row_stride(h, M, H, "h"), pq, ps,
+         s.shape[1])
 
 
 def add_rmsnorm_quant_alloc(x, res, gamma, eps, stream=None):
@@ -649,21 +681,20 @@ def _grouped_weight(qw, sw, offsets, name, N_at):
     block scales sw [E,N/128,K/128], for offsets [E+1]; returns (E, N, K)."""
     _want(qw, torch.uint8, 3, name)
     _dense(qw, name)
-    E, N, K = qw.shape if N_at == 1 else (qw.shape[1], qw.shape[2], qw.shape[0])
+    shape = qw.shape
+    E, N, K = shape if N_at == 1 else (shape[1], shape[2], shape[0])
     if _offsets(offsets) != E:
         raise ValueError("%s holds %d experts, offsets %d" % (name, E, offsets.numel() - 1))
-    _shape(sw, (E, _groups(N), _groups(K)), torch.float32, "sw")
-    _dense(sw, "sw")
+    _exact_dense(sw, (E, _groups(N), _groups(K)), torch.float32, "sw")
     return E, N, K
 
 
 def _grouped_rows(q, s, width, name_q, name_s):
     """Row operand q [M,width] with its 1x128 scales; returns M."""
     _want(q, torch.uint8, 2, name_q)
-    _dense(q, name_q); _dense(s, name_s)
     M = q.shape[0]
-    _shape(q, (M, width), torch.uint8, name_q)
-    _scales_1x128(s, _groups(width), M, name_s)
+    _exact_dense(q, (M, width), torch.uint8, name_q)
+    _scales_1x128(s, _groups(width), M, name_s); _dense(s, name_s)
     return M
 
 
@@ -673,11 +704,11 @@ def grouped_linear_fwd(qa, sa, qw, sw, offsets, y, stream=None):
     Rows of no expert are left as they are. offsets: int32 [E+1] on the device."""
     E, N, K = _grouped_weight(qw, sw, offsets, "qw", 1)
     M = _grouped_rows(qa, sa, K, "qa", "sa")
-    _shape(y, (M, N), torch.bfloat16, "y")
-    _together((qa, "qa"), (sa, "sa"), (qw, "qw"), (sw, "sw"), (offsets, "offsets"), (y, "y"))
-    _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, qa, _ptr(qa), _ptr(sa),
-         sa.shape[1], _ptr(qw), _ptr(sw), _ptr(offsets), E, M, N, K, _ptr(y),
-         _row_stride(y, "y"))
+    _exact(y, (M, N), torch.bfloat16, "y")
+    pa, psa, pw, psw, po, py = _pointers((qa, "qa"), (sa, "sa"), (qw, "qw"), (sw, "sw"),
+                                         (offsets, "offsets"), (y, "y"))
+    _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, qa, pa, psa,
+         sa.shape[1], pw, psw, po, E, M, N, K, py, _row_stride(y, M, N, "y"))
 
 
 def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
@@ -685,24 +716,22 @@ def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
     transposed and stacked, qwT [K,E,N]). Rows of no expert are left as they are."""
     E, N, K = _grouped_weight(qwT, sw, offsets, "qwT", 2)
     M = _grouped_rows(qdy, sdy, N, "qdy", "sdy")
-    _shape(dx, (M, K), torch.bfloat16, "dx")
-    _together((qdy, "qdy"), (sdy, "sdy"), (qwT, "qwT"), (sw, "sw"), (offsets, "offsets"),
-              (dx, "dx"))
-    _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, qdy, _ptr(qdy),
-         _ptr(sdy), sdy.shape[1], _ptr(qwT), _ptr(sw), _ptr(offsets), E, M, N, K, _ptr(dx),
-         _row_stride(dx, "dx"))
+    _exact(dx, (M, K), torch.bfloat16, "dx")
+    pa, psa, pw, psw, po, px = _pointers((qdy, "qdy"), (sdy, "sdy"), (qwT, "qwT"), (sw, "sw"),
+                                         (offsets, "offsets"), (dx, "dx"))
+    _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, qdy, pa, psa,
+         sdy.shape[1], pw, psw, po, E, M, N, K, px, _row_stride(dx, M, K, "dx"))
 
 
 def _grouped_columns(qT, sT, rows, name_q, name_s):
     """Transposed codes [rows,P] with their 128x1 scales [P/128,rows]; returns P."""
     _want(qT, torch.uint8, 2, name_q)
-    _dense(qT, name_q); _dense(sT, name_s)
     P = qT.shape[1]
     if P % 128:
         raise ValueError("%s must have a multiple of 128 columns, got %s" % (
             name_q, tuple(qT.shape)))
-    _shape(qT, (rows, P), torch.uint8, name_q)
-    _shape(sT, (P // 128, rows), torch.float32, name_s)
+    _exact_dense(qT, (rows, P), torch.uint8, name_q)
+    _exact_dense(sT, (P // 128, rows), torch.float32, name_s)
     return P
 
 
@@ -712,21 +741,19 @@ def grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, strea
     P >= grouped_padded_rows(M, E)."""
     _want(dy, torch.bfloat16, 2, "dy")
     E = _offsets(offsets)
-    M, N = dy.shape
+    M, N = shape = dy.shape
     lds_row = 0
     if (q_row is None) != (s_row is None):
         raise ValueError("q_row and s_row must be given together")
     if q_row is not None:
-        _dense(q_row, "q_row"); _dense(s_row, "s_row")
-        _shape(q_row, (M, N), torch.uint8, "q_row")
-        _scales_1x128(s_row, _groups(N), M, "s_row")
+        _exact_dense(q_row, shape, torch.uint8, "q_row")
+        _scales_1x128(s_row, _groups(N), M, "s_row"); _dense(s_row, "s_row")
         lds_row = s_row.shape[1]
     P = _grouped_columns(q_colT, s_col, N, "q_colT", "s_col")
-    _together((dy, "dy"), (offsets, "offsets"), (q_row, "q_row"), (s_row, "s_row"),
-              (q_colT, "q_colT"), (s_col, "s_col"))
+    pd, po, pq, ps, pqT, psT = _pointers((dy, "dy"), (offsets, "offsets"), (q_row, "q_row"),
+                                         (s_row, "s_row"), (q_colT, "q_colT"), (s_col, "s_col"))
     _run(_lib.fp8q_grouped_transpose_quant_bf16, "fp8q_grouped_transpose_quant_bf16", stream, dy,
-         _ptr(dy), _ptr(offsets), E, M, N, _row_stride(dy, "dy"), _ptr(q_row), _ptr(s_row),
-         lds_row, _ptr(q_colT), _ptr(s_col), P)
+         pd, po, E, M, N, _row_stride(dy, M, N, "dy"), pq, ps, lds_row, pqT, psT, P)
 
 
 def grouped_transpose_quant_bf16_alloc(dy, offsets, want_row=True, stream=None):
@@ -750,9 +777,10 @@ def grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream=None):
     K = q.shape[1]
     M = _grouped_rows(q, s, K, "q", "s")
     P = _grouped_columns(qT, sT, K, "qT", "sT")
-    _together((q, "q"), (s, "s"), (offsets, "offsets"), (qT, "qT"), (sT, "sT"))
+    pq, ps, po, pqT, psT = _pointers((q, "q"), (s, "s"), (offsets, "offsets"), (qT, "qT"),
+                                     (sT, "sT"))
     _run(_lib.fp8q_grouped_transpose_quant_fp8, "fp8q_grouped_transpose_quant_fp8", stream, q,
-         _ptr(q), _ptr(s), _ptr(offsets), E, M, K, s.shape[1], _ptr(qT), _ptr(sT), P)
+         pq, ps, po, E, M, K, s.shape[1], pqT, psT, P)
 
 
 def grouped_transpose_quant_fp8_alloc(q, s, offsets, stream=None):
@@ -776,15 +804,15 @@ def grouped_linear_wgrad(qdyT, sdy_c, qxT, sx_c, offsets, dw, stream=None):
             qdyT.shape[1], tuple(qxT.shape)))
     P = _grouped_columns(qdyT, sdy_c, N, "qdyT", "sdy_c")
     _grouped_columns(qxT, sx_c, K, "qxT", "sx_c")
+    E = _offsets(offsets)
     _want(dw, torch.bfloat16, 3, "dw")
-    E = dw.shape[0]
-    _shape(dw, (E, N, K), torch.bfloat16, "dw")
-    _dense(dw, "dw")
-    _offsets(offsets, E)
-    _together((qdyT, "qdyT"), (sdy_c, "sdy_c"), (qxT, "qxT"), (sx_c, "sx_c"),
-              (offsets, "offsets"), (dw, "dw"))
-    _run(_lib.fp8q_grouped_linear_wgrad, "fp8q_grouped_linear_wgrad", stream, qdyT, _ptr(qdyT),
-         _ptr(sdy_c), _ptr(qxT), _ptr(sx_c), _ptr(offsets), E, P, N, K, _ptr(dw), K)
+    if dw.shape[0] != E:
+        raise ValueError("dw holds %d experts, offsets %d" % (dw.shape[0], E))
+    _exact_dense(dw, (E, N, K), torch.bfloat16, "dw")
+    pa, psa, pb, psb, po, pw = _pointers((qdyT, "qdyT"), (sdy_c, "sdy_c"), (qxT, "qxT"),
+                                         (sx_c, "sx_c"), (offsets, "offsets"), (dw, "dw"))
+    _run(_lib.fp8q_grouped_linear_wgrad, "fp8q_grouped_linear_wgrad", stream, qdyT, pa, psa, pb,
+         psb, po, E, P, N, K, pw, K)
 
 
 def debug_wait_timeout(limit_ns: int, stream=None) -> int:

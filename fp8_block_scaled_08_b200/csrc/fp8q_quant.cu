@@ -907,9 +907,13 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   return r;
 }
 
-// Two BF16 pairs added, each sum formed in fp32 and rounded to BF16.
+// Two BF16 pairs added, each sum rounded once to BF16. That is bf16(fl32(a + b)) too: the
+// fp32 rounding in between cannot change the BF16 rounding of a sum of two 8-bit
+// significands (24 >= 2 * 8 + 2 bits make a double rounding innocuous).
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-  return pack_bf16x2(__fadd_rn(bf16_lo(a), bf16_lo(b)), __fadd_rn(bf16_hi(a), bf16_hi(b)));
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
   return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
@@ -918,46 +922,95 @@ __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
 
 // Residual addition + RMSNorm + quantization, one CTA per row: h = bf16(x + res) is formed
 // in registers, stored, and normalized from there, so each of x, res and h crosses HBM
-// once. kChunks 16-byte chunks per thread (H <= 8 * kChunks * threads).
-template <int kChunks>
-__global__ void __launch_bounds__(kNormThreads) add_rmsnorm_quant_cta_kernel(
+// once (7.03 bytes per element, which bounds it). Thread t owns the 8-element chunks t,
+// t + kThreads, ...: a half-warp holds one 1x128 group. A CTA loads its next row's inputs
+// before it waits for the sum of this one, and keeps its part of gamma.
+// kShare: one warp forms r for the CTA (its two fp64 divisions and square root cost as many
+// instructions per warp as half of the row's other work); without it every warp does,
+// which saves a barrier where the few rows leave most SMs idle.
+template <int kThreads, int kChunks, bool kShare, int kMinCtas = 1>
+__global__ void __launch_bounds__(kThreads, kMinCtas) add_rmsnorm_quant_kernel(
     const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ gamma, int64_t M,
     int64_t H, int64_t ldx, int64_t ldr, float eps, uint16_t* h, int64_t ldh,
     uint8_t* __restrict__ q, float* __restrict__ s, int64_t lds) {
-  __shared__ double red[kNormThreads / 32];
-  extern __shared__ uint4 gamma_sm[];  // H BF16 values, shared by every row
+  constexpr int kWarps = kThreads / 32;
+  __shared__ double red[2][kWarps];
+  __shared__ float r_sh[2];
   const int tid = threadIdx.x;
   const int lane = tid & 31, wid = tid >> 5;
-  const int64_t nch = H >> 3;
-  for (int64_t i = tid; i < nch; i += kNormThreads) gamma_sm[i] = ld_nc_v4(gamma + i * 8);
-  for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-    uint4 raw[kChunks];
+  const int nch = static_cast<int>(H >> 3);
+  int flip = 0;  // the shared words alternate, so a row needs no barrier behind it
+  uint4 nx[kChunks], nr[kChunks], gm[kChunks];  // the row to come, and gamma
+  auto load = [&](int64_t m) {
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const int64_t c = tid + j * kNormThreads;
+      const int c = tid + j * kThreads;
       if (c < nch) {
-        raw[j] = add_bf16x8(ld_stream_v4(x + m * ldx + c * 8), ld_stream_v4(res + m * ldr + c * 8));
-        *reinterpret_cast<uint4*>(h + m * ldh + c * 8) = raw[j];
+        nx[j] = ld_stream_v4(x + m * ldx + c * 8);
+        nr[j] = ld_stream_v4(res + m * ldr + c * 8);
       }
     }
-    double ss = sum_squares<kChunks>(raw, tid, kNormThreads, nch);
+  };
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(kFull, ss, off));
-    if (lane == 0) red[wid] = ss;
-    __syncthreads();
-    double tot = 0.0;
+  for (int j = 0; j < kChunks; ++j) nx[j] = nr[j] = gm[j] = make_uint4(0u, 0u, 0u, 0u);
+  load(blockIdx.x);  // the grid has at most M CTAs
 #pragma unroll
-    for (int w = 0; w < kNormThreads / 32; ++w) tot = __dadd_rn(tot, red[w]);
-    const float r = rstd_from_ss(tot, H, eps);
+  for (int j = 0; j < kChunks; ++j)
+    if (tid + j * kThreads < nch)
+      gm[j] = __ldg(reinterpret_cast<const uint4*>(gamma + (tid + j * kThreads) * 8));
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x, flip ^= 1) {
+    uint4 v[kChunks];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const int64_t c0 = static_cast<int64_t>(j) * kNormThreads + (tid & ~31);
-      if (c0 >= nch) break;  // warp-uniform; lanes past nch (a partial group) hold zeros
-      const int64_t c = tid + j * kNormThreads;
-      norm_quant_chunk(raw[j], reinterpret_cast<const uint16_t*>(gamma_sm), c, c < nch, r,
-                       q + m * H, s, lds, m, lane);
+      const int c = tid + j * kThreads;
+      v[j] = add_bf16x8(nx[j], nr[j]);
+      if (c < nch) *reinterpret_cast<uint4*>(h + m * ldh + c * 8) = v[j];
     }
-    __syncthreads();  // red is reused by the next row
+    if (kShare && m + gridDim.x < M) load(m + gridDim.x);
+    double ss = sum_squares<kChunks>(v, tid, kThreads, nch);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(kFull, ss, off));
+    if (lane == 0) red[flip][wid] = ss;
+    __syncthreads();
+    float r;
+    if (!kShare || wid == 0) {
+      double tot = lane < kWarps ? red[flip][lane] : 0.0;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1)
+        if (off < kWarps) tot = __dadd_rn(tot, __shfl_xor_sync(kFull, tot, off));
+      r = rstd_from_ss(__shfl_sync(kFull, tot, 0), H, eps);
+      if (kShare && lane == 0) r_sh[flip] = r;
+    }
+    if (kShare) {
+      __syncthreads();
+      r = r_sh[flip];
+    }
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int c = tid + j * kThreads;
+      if ((c & ~31) >= nch) break;  // warp-uniform; lanes past nch (a partial group) hold zeros
+      float xv[8], gv[8], b[8];
+      unpack_bf16x8(v[j], xv);
+      unpack_bf16x8(gm[j], gv);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float a0, a1;
+        mul2(a0, a1, xv[i], xv[i + 1], r, r);
+        mul2(b[i], b[i + 1], a0, a1, gv[i], gv[i + 1]);
+      }
+      const uint4 y = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]),
+                                 pack_bf16x2(b[4], b[5]), pack_bf16x2(b[6], b[7]));
+      uint32_t mx = bf16x2_maxabs_xs(bf16x2_maxabs_xs(y.x, y.y), bf16x2_maxabs_xs(y.z, y.w));
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1)
+        mx = bf16x2_maxabs_xs(mx, __shfl_xor_sync(kFull, mx, off));
+      const GroupScale g = group_scale_bf16(bf16x2_hmax_abs(mx));
+      const uint2 codes = __any_sync(kFull, g.small) ? codes8_words<true>(y, g) : codes8_words<false>(y, g);
+      if (c < nch) {
+        *reinterpret_cast<uint2*>(q + m * H + c * 8) = codes;
+        if ((lane & 15) == 0) s[(c >> 4) * lds + m] = g.s;
+      }
+    }
   }
 }
 
@@ -2011,7 +2064,11 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
     *abort_flag = 0;
     fence_barrier_init();
   }
-  int* const goff = reinterpret_cast<int*>(abort_flag + 4);
+  // grouped: first row and number of rows of the tile in each stage, written by the
+  // producer before it arrives on the stage's barrier (a search of the table by each of the
+  // sixteen consumer warps measured 71 us against XX for 16384 x 4096)
+  int2* const stage_rows = reinterpret_cast<int2*>(abort_flag + 2);
+  int* const goff = reinterpret_cast<int*>(stage_rows + kStages);
   int* const gfirst = goff + grp.experts + 1;
   if constexpr (kGrouped)
     group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
@@ -2019,17 +2076,6 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
   __syncthreads();
   const int64_t NB = (N + 127) >> 7;
   const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * NB;
-  // first row of row block mb, and one past its last row
-  auto block_rows = [&](int64_t mb, int64_t& r0, int64_t& r1) {
-    if constexpr (kGrouped) {
-      const int e = group_find(gfirst, grp.experts, static_cast<int>(mb));
-      r0 = goff[e] + 128 * (mb - gfirst[e]);
-      r1 = min(static_cast<int64_t>(goff[e + 1]), r0 + 128);
-    } else {
-      r0 = mb * 128;
-      r1 = M;
-    }
-  };
   if (warp == 16) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -2041,8 +2087,12 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         const uint32_t ph = static_cast<uint32_t>(i / kStages) & 1u;
         if (i >= kStages && !mbar_wait(empty + b, ph ^ 1u, ctl)) { ok = false; break; }
         const int64_t mb = t / NB, nb = t - mb * NB;
-        int64_t r0, r1;
-        block_rows(mb, r0, r1);
+        int64_t r0 = mb * 128;
+        if constexpr (kGrouped) {
+          const int e = group_find(gfirst, grp.experts, static_cast<int>(mb));
+          r0 = goff[e] + 128 * (mb - gfirst[e]);
+          stage_rows[b] = make_int2(static_cast<int>(r0), min(128, goff[e + 1] - static_cast<int>(r0)));
+        }
         mbar_arrive_expect_tx(full + b, kStageBytes);
         tma_load_2d(base + b * kStageBytes, &tmD, static_cast<int32_t>(nb * 128),
                     static_cast<int32_t>(r0), full + b);
@@ -2100,6 +2150,7 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4*>(row + ((j + lane) & 7) * 8);
       }
+      const int2 rows = kGrouped ? stage_rows[b] : make_int2(0, 0);
       const float amax = half_row_amax(w);
       __syncwarp();  // every lane's reads of the tile are complete (their values are used)
       if (lane == 0) mbar_arrive(empty + b);
@@ -2110,9 +2161,8 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         __syncwarp();
       }
       half_row_codes(w, g, out + rl * 128 + hh * 64, lane);
-      int64_t r0, r1;
-      block_rows(mb, r0, r1);
-      const int64_t m0 = r0 + warp * 16;
+      const int64_t m0 = (kGrouped ? rows.x : mb * 128) + warp * 16;
+      const int64_t r1 = kGrouped ? rows.x + rows.y : M;  // one past the tile's rows
       if (!kGrouped || m0 + 16 <= r1) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -2157,9 +2207,7 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
 #pragma unroll
       for (int k = 0; k < 32; ++k) w[k] = tw[k * 64];
       if constexpr (kGrouped) {  // rows past the group's end
-        int64_t r0, r1;
-        block_rows(t / NB, r0, r1);
-        const int valid = static_cast<int>(r1 - r0) - q4 * 32;
+        const int valid = stage_rows[b].y - q4 * 32;
         if (valid < 32) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) w[k] = k < valid ? w[k] : 0u;
@@ -2766,7 +2814,8 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
   extern __shared__ uint8_t smem_raw[];
   constexpr int kScRows = kGrouped ? 132 : 128;
   const TileSmem sm = carve_tiles(smem_raw, kGrouped ? kGroupedTileFP8 : kTileElems + 512);
-  int* const goff = sm.flag + 4;
+  int2* const tile_rows = reinterpret_cast<int2*>(sm.flag + 2);  // [2] first row, rows
+  int* const goff = reinterpret_cast<int*>(tile_rows + 2);
   int* const gfirst = goff + grp.experts + 1;
   if constexpr (kGrouped) {
     group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
@@ -2780,21 +2829,14 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
   const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * KB;
   const int64_t P = kGrouped ? grp.P : M;
   const int tid = threadIdx.x;
-  // first row of row block mb, and (grouped) how many rows it has
-  auto block_rows = [&](int64_t mb, int& rows) -> int32_t {
-    if constexpr (kGrouped) {
-      const int e = group_find(gfirst, grp.experts, static_cast<int>(mb));
-      const int r0 = goff[e] + 128 * (static_cast<int>(mb) - gfirst[e]);
-      rows = min(128, goff[e + 1] - r0);
-      return r0;
-    } else {
-      rows = 128;
-      return static_cast<int32_t>(mb * 128);
-    }
-  };
   auto issue = [&](int b, int64_t t) {
-    int rows;
-    const int32_t mx = block_rows(t / KB, rows), kx = static_cast<int32_t>(t % KB);
+    int32_t mx = static_cast<int32_t>((t / KB) * 128);
+    const int32_t kx = static_cast<int32_t>(t % KB);
+    if constexpr (kGrouped) {
+      const int mb = static_cast<int>(t / KB), e = group_find(gfirst, grp.experts, mb);
+      mx = goff[e] + 128 * (mb - gfirst[e]);
+      tile_rows[b] = make_int2(mx, min(128, goff[e + 1] - mx));
+    }
     mbar_arrive_expect_tx(sm.bar + b, kTileElems + 4 * kScRows);
     tma_load_2d(sm.buf[b], &tmQ, kx * 128, mx, sm.bar + b);
     tma_load_2d(sm.buf[b] + kTileElems, &tmS, kGrouped ? mx & ~3 : mx, kx, sm.bar + b);
@@ -2811,7 +2853,10 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const int64_t mb = t / KB, kb = t % KB;
     float x0[32], x1[32];
     int grows = 128;
-    if constexpr (kGrouped) rsc += block_rows(mb, grows) & 3;
+    if constexpr (kGrouped) {
+      rsc += tile_rows[i & 1].x & 3;
+      grows = tile_rows[i & 1].y;
+    }
 #pragma unroll
     for (int r4 = 0; r4 < 32; r4 += 4) {
       float sr[4];
@@ -3570,13 +3615,27 @@ extern "C" fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t*
   const int sms = sm100_sm_count();
   if (!sms) return FP8Q_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t gsm = static_cast<size_t>(H) * 2;  // gamma in shared memory
-  const int64_t grid = M < static_cast<int64_t>(sms) * 64 ? M : static_cast<int64_t>(sms) * 64;
-  auto kern = H <= 2 * 8 * kNormThreads   ? add_rmsnorm_quant_cta_kernel<2>
-              : H <= 4 * 8 * kNormThreads ? add_rmsnorm_quant_cta_kernel<4>
-                                          : add_rmsnorm_quant_cta_kernel<kNormMaxChunks>;
-  kern<<<static_cast<int>(grid), kNormThreads, gsm, st>>>(x, res, gamma, M, H, ldx, ldres, eps, h,
-                                                          ldh, q, s, lds);
+  // Few rows: as many threads as the row has chunks, every warp forming r. From two rows per
+  // SM on: fewer threads with two or four chunks, one of the warps forming r.
+  struct Choice {
+    decltype(&add_rmsnorm_quant_kernel<128, 1, false>) kern;
+    int threads, ctas;  // CTAs of an SM
+  };
+  const bool many = M >= 2 * static_cast<int64_t>(sms);
+  const Choice few_k = H <= 1024   ? Choice{add_rmsnorm_quant_kernel<128, 1, false>, 128, 1}
+                       : H <= 4096 ? Choice{add_rmsnorm_quant_kernel<512, 1, false>, 512, 1}
+                       : H <= 8192 ? Choice{add_rmsnorm_quant_kernel<1024, 1, false>, 1024, 1}
+                                   : Choice{add_rmsnorm_quant_kernel<1024, 2, false>, 1024, 1};
+  const Choice many_k = H <= 1024   ? Choice{add_rmsnorm_quant_kernel<128, 1, true, 8>, 128, 8}
+                        : H <= 2048 ? Choice{add_rmsnorm_quant_kernel<128, 2, true, 6>, 128, 6}
+                        : H <= 4096 ? Choice{add_rmsnorm_quant_kernel<128, 4, true, 4>, 128, 4}
+                        : H <= 6144 ? Choice{add_rmsnorm_quant_kernel<256, 3, true, 2>, 256, 2}
+                        : H <= 8192 ? Choice{add_rmsnorm_quant_kernel<256, 4, true, 2>, 256, 2}
+                                    : Choice{add_rmsnorm_quant_kernel<512, 4, true, 1>, 512, 1};
+  const Choice k = many ? many_k : few_k;
+  const int64_t grid = many ? std::min<int64_t>(M, static_cast<int64_t>(sms) * k.ctas) : M;
+  k.kern<<<static_cast<int>(grid), k.threads, 0, st>>>(x, res, gamma, M, H, ldx, ldres, eps, h, ldh,
+                                                       q, s, lds);
   return launch_status("add_rmsnorm_quant launch");
 }
 
@@ -3609,7 +3668,8 @@ extern "C" fp8q_status fp8q_grouped_transpose_quant_bf16(
   if (!err) return FP8Q_ERR_CUDA;
   const int64_t tiles = grouped_padded_rows(M, E) / 128 * ((N + 127) / 128);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t smem = a6_smem<TileGrad>() + group_table_bytes(static_cast<int>(E));
+  const size_t smem = a6_smem<TileGrad>() + 8 * A6Layout<TileGrad>::kStages +
+                      group_table_bytes(static_cast<int>(E));
   const TileGroups grp{offsets, static_cast<int>(E), P, q_row};
   auto kern = q_row ? a6_tile_kernel<TileGrad, true, true> : a6_tile_kernel<TileGrad, false, true>;
   static std::atomic<int> smem_ok[2][64];
