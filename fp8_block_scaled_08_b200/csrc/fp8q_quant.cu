@@ -1302,11 +1302,6 @@ __device__ __forceinline__ void tile_cols_bf16(const uint16_t* Ts, float* red, b
 
 // Shared memory of the FP8 tile kernel (a8): two (16 KB codes + 512 B row scales) buffers.
 constexpr size_t kTileSmemFP8 = 1024 + 2 * (kTileElems + 512) + 4 * 128 * 4 + 64;
-// Grouped: 132 row scales, rounded up to the 128 bytes a tensor copy's destination needs.
-constexpr int kGroupedTileFP8 = kTileElems + 640;
-constexpr size_t grouped_tile_smem_fp8(int E) {
-  return 1024 + 2 * kGroupedTileFP8 + 4 * 128 * 4 + 64 + group_table_bytes(E);
-}
 
 __device__ __forceinline__ TileSmem carve_tiles(uint8_t* raw, int buf_bytes,
                                                int red_floats = 4 * 128) {
@@ -2066,7 +2061,7 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
   }
   // grouped: first row and number of rows of the tile in each stage, written by the
   // producer before it arrives on the stage's barrier (a search of the table by each of the
-  // sixteen consumer warps measured 71 us against XX for 16384 x 4096)
+  // sixteen consumer warps measured 71 us against 60 for 16384 x 4096)
   int2* const stage_rows = reinterpret_cast<int2*>(abort_flag + 2);
   int* const goff = reinterpret_cast<int*>(stage_rows + kStages);
   int* const gfirst = goff + grp.experts + 1;
@@ -2803,43 +2798,23 @@ __global__ void __launch_bounds__(256) dgamma_round_kernel(const unsigned long l
 // quot's q + (x - q s) y with y = fl32(1/s) and q = fl32(x y) is fl32(x / s) for every
 // x and s of fp32 without underflow (Markstein's theorem: y within half an ulp of 1/s,
 // q within one ulp of x/s, the residual exact by the FMA). Scales below 2^-80 divide.
-// kGrouped: the 128-row blocks are the experts' groups (they restart at each expert; rows
-// past a group's end count as zeros), and qT's rows are grp.P long. A group may start at
-// any row, so its row scales come as a copy of 132 from the multiple of 4 before it.
-template <bool kGrouped>
 __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmS, int64_t M,
     int64_t K, uint8_t* __restrict__ qT, float* __restrict__ sT, unsigned* err,
-    uint64_t limit_ns, const TileGroups grp) {
+    uint64_t limit_ns) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kScRows = kGrouped ? 132 : 128;
-  const TileSmem sm = carve_tiles(smem_raw, kGrouped ? kGroupedTileFP8 : kTileElems + 512);
-  int2* const tile_rows = reinterpret_cast<int2*>(sm.flag + 2);  // [2] first row, rows
-  int* const goff = reinterpret_cast<int*>(tile_rows + 2);
-  int* const gfirst = goff + grp.experts + 1;
-  if constexpr (kGrouped) {
-    group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
-                     groups_of_rows);
-    __syncthreads();
-  }
+  const TileSmem sm = carve_tiles(smem_raw, kTileElems + 512);
   __shared__ int abort_flag;
   const WaitCtl ctl{&abort_flag, err, limit_ns};
   if (threadIdx.x == 0) abort_flag = 0;
   const int64_t KB = (K + 127) >> 7;
-  const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * KB;
-  const int64_t P = kGrouped ? grp.P : M;
+  const int64_t tiles = ((M + 127) >> 7) * KB;
   const int tid = threadIdx.x;
   auto issue = [&](int b, int64_t t) {
-    int32_t mx = static_cast<int32_t>((t / KB) * 128);
-    const int32_t kx = static_cast<int32_t>(t % KB);
-    if constexpr (kGrouped) {
-      const int mb = static_cast<int>(t / KB), e = group_find(gfirst, grp.experts, mb);
-      mx = goff[e] + 128 * (mb - gfirst[e]);
-      tile_rows[b] = make_int2(mx, min(128, goff[e + 1] - mx));
-    }
-    mbar_arrive_expect_tx(sm.bar + b, kTileElems + 4 * kScRows);
+    const int32_t mx = static_cast<int32_t>((t / KB) * 128), kx = static_cast<int32_t>(t % KB);
+    mbar_arrive_expect_tx(sm.bar + b, kTileElems + 512);
     tma_load_2d(sm.buf[b], &tmQ, kx * 128, mx, sm.bar + b);
-    tma_load_2d(sm.buf[b] + kTileElems, &tmS, kGrouped ? mx & ~3 : mx, kx, sm.bar + b);
+    tma_load_2d(sm.buf[b] + kTileElems, &tmS, mx, kx, sm.bar + b);
   };
   tiles_prologue(sm, tiles, issue);
   const int cp = tid & 63, rq = tid >> 6;
@@ -2852,21 +2827,10 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const float* rsc = reinterpret_cast<const float*>(Tq + kTileElems);
     const int64_t mb = t / KB, kb = t % KB;
     float x0[32], x1[32];
-    int grows = 128;
-    if constexpr (kGrouped) {
-      rsc += tile_rows[i & 1].x & 3;
-      grows = tile_rows[i & 1].y;
-    }
 #pragma unroll
     for (int r4 = 0; r4 < 32; r4 += 4) {
-      float sr[4];
-      if constexpr (kGrouped) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sr[k] = rsc[32 * rq + r4 + k];  // broadcast
-      } else {
-        const float4 sr4 = *reinterpret_cast<const float4*>(rsc + 32 * rq + r4);  // broadcast
-        sr[0] = sr4.x; sr[1] = sr4.y; sr[2] = sr4.z; sr[3] = sr4.w;
-      }
+      const float4 sr4 = *reinterpret_cast<const float4*>(rsc + 32 * rq + r4);  // broadcast
+      const float sr[4] = {sr4.x, sr4.y, sr4.z, sr4.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = r4 + k;
@@ -2874,15 +2838,6 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
         const float2 d = e4m3x2_to_f32(two);
         x0[r] = __fmul_rn(sr[k], d.x);
         x1[r] = __fmul_rn(sr[k], d.y);
-      }
-    }
-    if constexpr (kGrouped) {
-      if (32 * rq + 32 > grows) {  // rows past the group's end
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          x0[r] = 32 * rq + r < grows ? x0[r] : 0.0f;
-          x1[r] = 32 * rq + r < grows ? x1[r] : 0.0f;
-        }
       }
     }
     float c0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -2903,7 +2858,7 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     const GroupScale g0 = group_scale_fma(a0), g1 = group_scale_fma(a1);
     const float s0 = g0.s, s1 = g1.s;
     // a partial tile (ragged M or K) arrived zero-filled; store only its valid part
-    const int rows = !kGrouped && M - mb * 128 < 128 ? static_cast<int>(M - mb * 128) : 128;
+    const int rows = M - mb * 128 < 128 ? static_cast<int>(M - mb * 128) : 128;
     const bool col_ok = kb * 128 + 2 * cp < K;  // K is even: the pair is in or out
     if (rq == 0 && col_ok)
       *reinterpret_cast<float2*>(sT + mb * K + kb * 128 + 2 * cp) = make_float2(s0, s1);
@@ -2930,9 +2885,9 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
         o1[k] = cvt_e4m3x4(t1[0], t1[1], t1[2], t1[3]);
       }
     }
-    uint8_t* dst = qT + (kb * 128) * P + mb * 128;
-    uint4* d0 = reinterpret_cast<uint4*>(dst + (2 * cp) * P + 32 * rq);
-    uint4* d1 = reinterpret_cast<uint4*>(dst + (2 * cp + 1) * P + 32 * rq);
+    uint8_t* dst = qT + (kb * 128) * M + mb * 128;
+    uint4* d0 = reinterpret_cast<uint4*>(dst + (2 * cp) * M + 32 * rq);
+    uint4* d1 = reinterpret_cast<uint4*>(dst + (2 * cp + 1) * M + 32 * rq);
     if (col_ok && 32 * rq < rows) {  // rows is a multiple of 16
       d0[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
       d1[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
@@ -2943,6 +2898,268 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
     }
   }
   if (t < tiles) tiles_drain(sm, t, tiles, i, limit_ns);
+}
+
+// a8 for a grouped call, without a barrier between warps: the 128-row blocks are the
+// experts' groups (they restart at each expert; rows past a group's end count as zeros).
+//   A group of four warps owns two stages of the ring (a 128x128 code tile, 128-byte
+//   swizzle, and its row scales) and takes every kRqGroups-th tile of the CTA; a warp takes
+//   32 columns over all 128 rows, so a column's maximum needs only shuffles: lane 8g + c
+//   holds columns 4c .. 4c + 3 (one word a row) of rows 8j + 2g and 8j + 2g + 1 (j < 16);
+//   with the swizzle the four g read four different pairs of 16-byte chunks, free of bank
+//   conflicts. The 32 words stay in registers; the products s * dec(q) are formed twice
+//   (for the maximum and for the codes), since 128 of them would not fit. Codes of 8 rows x 4 columns move between the four g by a 4x4 transpose of
+//   halfwords (two shuffles), after which lane 8g + c holds column 4c + g in row order; it
+//   stages it for the warp's tensor store of 32 columns x 128 codes (stored from registers,
+//   every lane its own 128-byte line, the stores took about 15 us of the memory pipe).
+//   The last warp is the producer. A group may start at any row, so its row scales come as
+//   a copy of 132 from the multiple of 4 before it.
+// Latency bounds the dense kernel (two CTA barriers a tile, 14.6 warps an SM, 0.32 of the
+// issue slots at 8192 x 4096): its layout took 54.9 us here at 16384 x 4096, this one
+// 42.7 us (3.3 TB/s), 17.7 of them the reads alone; now the instructions bound it (12 per
+// element, 0.6 of the issue slots). Rolled-up loops that read the words twice took 50 us,
+// four or six groups of warps 43-50 us.
+constexpr int kRqGroups = 3;  // consumer groups of four warps
+constexpr int kRqStages = 2 * kRqGroups;
+constexpr int kRqThreads = 32 * (4 * kRqGroups + 1);
+constexpr uint32_t kRqTile = 128 * 128;
+constexpr uint32_t kRqScales = 640;  // 132 row scales; copies need 128-byte destinations
+constexpr uint32_t kRqOut = 32 * 128;  // a warp's transposed codes
+constexpr uint32_t kRqOffOut = kRqStages * kRqTile;
+constexpr uint32_t kRqOffScales = kRqOffOut + 4 * kRqGroups * kRqOut;
+constexpr uint32_t kRqOffRows = kRqOffScales + kRqStages * kRqScales;  // int2 per stage
+constexpr uint32_t kRqOffBar = kRqOffRows + kRqStages * 8;
+constexpr uint32_t kRqOffTab = kRqOffBar + 2 * kRqStages * 8 + 16;
+constexpr size_t requant_smem(int E) { return 1024 + kRqOffTab + group_table_bytes(E); }
+static_assert(requant_smem(kMaxExperts) <= 232448, "shared memory budget of one sm_100 CTA");
+
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
+// The four products s * dec(q) of a word of codes, each rounded to fp32.
+__device__ __forceinline__ void dequant4(uint32_t w, float s, float (&x)[4]) {
+  const float2 a = e4m3x2_to_f32(static_cast<uint16_t>(w));
+  const float2 b = e4m3x2_to_f32(static_cast<uint16_t>(w >> 16));
+  mul2(x[0], x[1], a.x, a.y, s, s);
+  mul2(x[2], x[3], b.x, b.y, s, s);
+}
+
+// Four codes of a word: requantized with the columns' scales (none of them tiny). The
+// quotient is quot's with the residual the other way round (x - q s, no negations), which
+// turns -0 into +0; the scales are positive, so a code's sign is that of the code it came
+// from.
+__device__ __forceinline__ uint32_t requant4(uint32_t w, float s, const GroupScale (&g)[4]) {
+  float x[4], t[4];
+  dequant4(w, s, x);
+#pragma unroll
+  for (int c = 0; c < 4; c += 2) {
+    mul2(t[c], t[c + 1], x[c], x[c + 1], g[c].rs, g[c + 1].rs);
+    fma2(x[c], x[c + 1], t[c], t[c + 1], g[c].ns, g[c + 1].ns);
+    fma2(t[c], t[c + 1], x[c], x[c + 1], g[c].rs, g[c + 1].rs);
+  }
+  return cvt_e4m3x4(t[0], t[1], t[2], t[3]) | (w & 0x80808080u);
+}
+
+// 8 rows x 32 columns of codes: ca and cb hold columns 4c .. 4c + 3 of rows 2g and 2g + 1
+// (lane 8g + c); o0 and o1 become rows 0-3 and 4-7 of column 4c + g.
+struct RowsToColumns {
+  uint32_t keep, send, sel0, sel1;
+  bool upper;
+  __device__ __forceinline__ explicit RowsToColumns(int gr) {
+    keep = (gr & 1) ? 0x7632u : 0x5410u;
+    send = keep ^ 0x2222u;
+    sel0 = gr == 0 ? 0x5410u : gr == 1 ? 0x1054u : gr == 2 ? 0x7632u : 0x3276u;
+    sel1 = sel0 ^ 0x2222u;
+    upper = gr & 2;
+  }
+  __device__ __forceinline__ void operator()(uint32_t ca, uint32_t cb, uint32_t& o0,
+                                             uint32_t& o1) const {
+    const uint32_t lo = byte_perm(ca, cb, 0x5140u), hi = byte_perm(ca, cb, 0x7362u);
+    const uint32_t a = upper ? hi : lo;
+    const uint32_t b = __shfl_xor_sync(kFull, upper ? lo : hi, 16);
+    const uint32_t mine = byte_perm(a, b, keep);
+    const uint32_t other = __shfl_xor_sync(kFull, byte_perm(a, b, send), 8);
+    o0 = byte_perm(mine, other, sel0);
+    o1 = byte_perm(mine, other, sel1);
+  }
+};
+
+// A warp's tile by IEEE division, for a warp that holds a column with a tiny scale: kept
+// out of line and rolled up, away from the registers of the usual path.
+__device__ __noinline__ void requant_tile_div(const uint8_t* worda, const uint8_t* wordb,
+                                              const float* rsc, float4 gs, int rows, int gr,
+                                              uint8_t* orow, int col) {
+  const RowsToColumns to_columns(gr);
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j) {
+    uint32_t c[2], o[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      float x[4];
+      dequant4(*reinterpret_cast<const uint32_t*>((b ? wordb : worda) + j * 1024), rsc[8 * j + b], x);
+      c[b] = cvt_e4m3x4(__fdiv_rn(x[0], gs.x), __fdiv_rn(x[1], gs.y), __fdiv_rn(x[2], gs.z),
+                        __fdiv_rn(x[3], gs.w));
+      if (8 * j + 2 * gr + b >= rows) c[b] = 0u;
+    }
+    to_columns(c[0], c[1], o[0], o[1]);
+    *reinterpret_cast<uint2*>(orow + (((j >> 1) ^ (col & 7)) << 4) + 8 * (j & 1)) = make_uint2(o[0], o[1]);
+  }
+}
+
+__global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
+    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmS,
+    const __grid_constant__ CUtensorMap tmQT, int64_t M, int64_t K, float* __restrict__ sT,
+    unsigned* err, uint64_t limit_ns, const TileGroups grp) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  int2* stage_rows = reinterpret_cast<int2*>(base + kRqOffRows);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + kRqOffBar);
+  uint64_t* empty = full + kRqStages;
+  int* abort_flag = reinterpret_cast<int*>(empty + kRqStages);
+  int* off = reinterpret_cast<int*>(base + kRqOffTab);
+  int* first = off + grp.experts + 1;
+  const WaitCtl ctl{abort_flag, err, limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < kRqStages; ++b) {
+      mbar_init(full + b, 1);
+      mbar_init(empty + b, 4);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  group_table_fill(off, first, grp.offsets, grp.experts, static_cast<int>(M), err, groups_of_rows);
+  __syncthreads();
+  const int64_t KB = (K + 127) >> 7;
+  const int64_t tiles = first[grp.experts] * KB;
+  if (warp == 4 * kRqGroups) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t issued = 0, par = 0;  // bit b: stage b has a copy issued / its parity
+      bool ok = true;
+      int i = 0;
+      for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+        const int n = i / kRqGroups;  // the tile's number within its group
+        const int b = 2 * (i % kRqGroups) + (n & 1);
+        const uint32_t ph = static_cast<uint32_t>(n >> 1) & 1u;
+        const int mb = static_cast<int>(t / KB), kx = static_cast<int>(t - mb * KB);
+        const int e = group_find(first, grp.experts, mb);
+        const int r0 = off[e] + 128 * (mb - first[e]);
+        if (n >= 2 && !mbar_wait(empty + b, ph ^ 1u, ctl)) { ok = false; break; }
+        stage_rows[b] = make_int2(r0, min(128, off[e + 1] - r0));
+        mbar_arrive_expect_tx(full + b, kRqTile + 132 * 4);
+        tma_load_2d(base + b * kRqTile, &tmQ, kx * 128, r0, full + b);
+        tma_load_2d(base + kRqOffScales + b * kRqScales, &tmS, r0 & ~3, kx, full + b);
+        issued |= 1u << b;
+        par = (par & ~(1u << b)) | (ph << b);
+      }
+      if (!ok) {  // let every copy already issued land before the CTA exits
+        for (int b = 0; b < kRqStages; ++b) {
+          if (!((issued >> b) & 1u)) continue;
+          const uint32_t a = smem_u32(full + b);
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try_wait(a, (par >> b) & 1u))
+            if (global_timer_ns() - t0 > limit_ns) break;
+        }
+      }
+    }
+    return;
+  }
+  // -------------------------------------------------------------- consumers
+  const int grp4 = warp >> 2, gr = lane >> 3, cw = lane & 7;
+  const RowsToColumns to_columns(gr);
+  // this lane's column after the transpose, and its row of the warp's staging tile (128-byte
+  // swizzle: the 16-byte writes of a warp take 4 wavefronts, the least possible)
+  const int col = 4 * cw + gr;
+  uint8_t* out = base + kRqOffOut + warp * kRqOut;
+  uint8_t* orow = out + col * 128;
+  const int chunk = 2 * (warp & 3) + (cw >> 2);
+  const uint32_t offa = 2 * gr * 128 + ((chunk ^ (2 * gr)) << 4) + (cw & 3) * 4;
+  const uint32_t offb = (2 * gr + 1) * 128 + ((chunk ^ (2 * gr + 1)) << 4) + (cw & 3) * 4;
+  int n = 0;
+  for (int64_t t = blockIdx.x + static_cast<int64_t>(grp4) * gridDim.x; t < tiles;
+       t += static_cast<int64_t>(kRqGroups) * gridDim.x, ++n) {
+    const int b = 2 * grp4 + (n & 1);
+    if (!mbar_wait_warp(full + b, static_cast<uint32_t>(n >> 1) & 1u, ctl)) break;
+    const int2 rr = stage_rows[b];
+    const uint8_t* tile = base + b * kRqTile;
+    const float* rsc = reinterpret_cast<const float*>(base + kRqOffScales + b * kRqScales) +
+                       (rr.x & 3) + 2 * gr;
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      w[2 * j] = *reinterpret_cast<const uint32_t*>(tile + offa + j * 1024);
+      w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(tile + offb + j * 1024);
+    }
+    if (rr.y < 128) {  // past the group's end: rows of the next expert, or of nobody
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        w[2 * j] = 8 * j + 2 * gr < rr.y ? w[2 * j] : 0u;
+        w[2 * j + 1] = 8 * j + 2 * gr + 1 < rr.y ? w[2 * j + 1] : 0u;
+      }
+    }
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float xa[4], xb[4];
+      dequant4(w[2 * j], rsc[8 * j], xa);
+      dequant4(w[2 * j + 1], rsc[8 * j + 1], xb);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) m[c] = fmaxf(fmaxf(m[c], fabsf(xa[c])), fabsf(xb[c]));
+    }
+    GroupScale g[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      m[c] = fmaxf(m[c], __shfl_xor_sync(kFull, m[c], 8));
+      m[c] = fmaxf(m[c], __shfl_xor_sync(kFull, m[c], 16));
+      g[c] = group_scale_fma(m[c]);
+    }
+    const int64_t mb = t / KB, kb = t - mb * KB;
+    const int64_t c0 = kb * 128 + 32 * (warp & 3) + 4 * cw;
+    if (gr == 0 && c0 < K)  // K is a multiple of 16: the four columns are in or out
+      *reinterpret_cast<float4*>(sT + mb * K + c0) = make_float4(g[0].s, g[1].s, g[2].s, g[3].s);
+    if (lane == 0) tma_store_wait_read();  // the previous tile's codes have left
+    __syncwarp();
+    if (__any_sync(kFull, g[0].small || g[1].small || g[2].small || g[3].small)) {
+      requant_tile_div(tile + offa, tile + offb, rsc, make_float4(g[0].s, g[1].s, g[2].s, g[3].s),
+                       rr.y, gr, orow, col);
+    } else {
+      // the products are formed again, not kept: hide that the words are the same
+#pragma unroll
+      for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(w[j]));
+#pragma unroll
+      for (int j2 = 0; j2 < 8; ++j2) {
+        uint32_t o[4];
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = 2 * j2 + jj;
+          uint32_t ca = requant4(w[2 * j], rsc[8 * j], g);
+          uint32_t cb = requant4(w[2 * j + 1], rsc[8 * j + 1], g);
+          if (rr.y < 128) {  // past the group's end: zero whatever the scale beside it is
+            ca = 8 * j + 2 * gr < rr.y ? ca : 0u;
+            cb = 8 * j + 2 * gr + 1 < rr.y ? cb : 0u;
+          }
+          to_columns(ca, cb, o[2 * jj], o[2 * jj + 1]);
+        }
+        *reinterpret_cast<uint4*>(orow + ((j2 ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();  // every lane's reads of the stage are complete, its codes are staged
+    if (lane == 0) {
+      mbar_arrive(empty + b);
+      const int64_t cb = kb * 128 + 32 * (warp & 3);
+      if (cb < K) {  // the copy clips a ragged K
+        tma_store_2d(&tmQT, out, static_cast<int32_t>(mb * 128), static_cast<int32_t>(cb));
+        tma_store_commit();
+      }
+    }
+  }
+  if (lane == 0) tma_store_wait_all();
 }
 
 // a2 on a tile ring. The block scale is shared by a block and its transpose, so qT is the
@@ -3409,10 +3626,10 @@ extern "C" fp8q_status fp8q_transpose_quant_fp8(const uint8_t* q, const float* s
   unsigned* err = device_error_word();
   if (!err) return FP8Q_ERR_CUDA;
   static std::atomic<int> occ[64];
-  const int per_sm = resident_ctas(transpose_quant_fp8_kernel<false>, 256, kTileSmemFP8, occ);
-  transpose_quant_fp8_kernel<false><<<grid_for(((M + 127) / 128) * KB, per_sm), 256, kTileSmemFP8,
+  const int per_sm = resident_ctas(transpose_quant_fp8_kernel, 256, kTileSmemFP8, occ);
+  transpose_quant_fp8_kernel<<<grid_for(((M + 127) / 128) * KB, per_sm), 256, kTileSmemFP8,
                                static_cast<cudaStream_t>(stream)>>>(tmq, tms, M, K, qT, sT, err,
-                                                                    kWaitLimitNs, TileGroups{});
+                                                                    kWaitLimitNs);
   return launch_status("transpose_quant_fp8 launch");
 }
 
@@ -3694,22 +3911,22 @@ extern "C" fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const 
     return FP8Q_ERR_ALIGN;
   if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
   const int64_t KB = (K + 127) / 128;
-  CUtensorMap tmq, tms;
+  CUtensorMap tmq, tms, tmqt;
   if (!encode_tmap_2d(&tmq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, M, K, 128, 128,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tmap_2d(&tms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, s, M, KB, lds * 4, 132, 1,
-                      CU_TENSOR_MAP_SWIZZLE_NONE))
+                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_tmap_2d(&tmqt, CU_TENSOR_MAP_DATA_TYPE_UINT8, qT, P, K, P, 128, 32,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
     return FP8Q_ERR_UNSUPPORTED;
   unsigned* err = device_error_word();
   if (!err) return FP8Q_ERR_CUDA;
   const int64_t tiles = grouped_padded_rows(M, E) / 128 * KB;
-  const size_t smem = grouped_tile_smem_fp8(static_cast<int>(E));
-  static std::atomic<int> occ[64];
-  const int per_sm = resident_ctas(transpose_quant_fp8_kernel<true>, 256,
-                                   grouped_tile_smem_fp8(kMaxExperts), occ);
+  static std::atomic<int> smem_ok[64];
+  if (!allow_max_smem(grouped_requant_kernel, smem_ok)) return FP8Q_ERR_CUDA;
   const TileGroups grp{offsets, static_cast<int>(E), P, nullptr};
-  transpose_quant_fp8_kernel<true><<<grid_for(tiles, per_sm), 256, smem,
-                                     static_cast<cudaStream_t>(stream)>>>(
-      tmq, tms, M, K, qT, sT, err, kWaitLimitNs, grp);
+  grouped_requant_kernel<<<grid_for(tiles, 1), kRqThreads, requant_smem(static_cast<int>(E)),
+                           static_cast<cudaStream_t>(stream)>>>(tmq, tms, tmqt, M, K, sT, err,
+                                                                kWaitLimitNs, grp);
   return launch_status("grouped_transpose_quant_fp8 launch");
 }

@@ -292,6 +292,38 @@ def test_transpose_quant_fp8(fq, oracle_mod, name, K):
     assert torch.all(qT[:, 128 * g:] == 77) and torch.all(sT[g:] == -1.0)
 
 
+def test_tiny_scales(fq, oracle_mod):
+    """Columns and rows whose scale is below 2^-80 take the kernels' division path, beside
+    others that do not."""
+    off, M, E = route("ragged")
+    N = 384
+    x = workloads.activations_bf16((M, N), 0, 3065, DEV)
+    x[:, 5:300:7] *= 1e-30
+    x[:, 128:256] *= 1e-33
+    x[3:40] *= 1e-28
+    o = dev_offsets(off)
+    P = fq.grouped_padded_rows(M, E)
+    q = torch.full((M, N), 77, dtype=torch.uint8, device=DEV)
+    s = torch.full((N // 128, fq.lds_for(M)), -1.0, device=DEV)
+    qT = torch.full((N, P), 77, dtype=torch.uint8, device=DEV)
+    sT = torch.full((P // 128, N), -1.0, device=DEV)
+    fq.grouped_transpose_quant_bf16(x, o, q, s, qT, sT)
+    check_rows_and_columns(oracle_mod, x, off, q, s, qT, sT)
+    qa, sa = fq.quant_act_1x128_alloc(x)
+    xT, xs = fq.grouped_transpose_quant_fp8_alloc(qa, sa, o)
+    g = 0
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        rqT, rsT = oracle_mod.transpose_quant_fp8(np_u8(qa[lo:hi]),
+                                                  np.ascontiguousarray(np_f32(sa)[:, lo:hi]))
+        assert_codes_equal(xT[:, 128 * g:128 * g + hi - lo], rqT, "columns of %d" % e)
+        n = -(-(hi - lo) // 128)
+        assert_scales_equal(xs[g:g + n], rsT, "column scales of %d" % e)
+        g += n
+
+
 def test_values_of_other_experts_do_not_leak(fq, oracle_mod):
     """NaN in the neighbours' rows (and in nobody's) changes nothing in an expert's groups."""
     off, M, E = route("spare")
