@@ -588,15 +588,24 @@ def _pointers(*named):
     dev = named[0][0].get_device()
     if dev < 0:
         raise ValueError("libfp8q takes CUDA tensors (device pointers)")
-    out = []
     for t, n in named:
-        if t is None:
-            out.append(None)
-        elif t.get_device() == dev:
-            out.append(t.data_ptr())
-        else:
+        if t is not None and t.get_device() != dev:
             raise ValueError("%s must be on cuda:%d, got %s" % (n, dev, t.device))
-    return out
+    return [None if t is None else t.data_ptr() for t, _ in named]
+
+
+_T, _BF16, _U8, _F32 = torch.Tensor, torch.bfloat16, torch.uint8, torch.float32
+
+
+def _scales_dense(s, groups, rows, name):
+    """Dense 1x128 scales fp32 [groups, lds >= rows]; returns lds."""
+    if isinstance(s, torch.Tensor) and s.dtype == _F32 and s.dim() == 2 and s.is_contiguous():
+        g, lds = s.shape
+        if g == groups and lds >= rows:
+            return lds
+    _scales_1x128(s, groups, rows, name)
+    _dense(s, name)
+    return s.shape[1]
 
 
 def _exact(t, shape, dtype, name):
@@ -637,18 +646,24 @@ def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
     """a3 behind a residual addition: h = bf16(x + res) [M,H] (may be x or res itself), then
     RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]. Its backward is
     rmsnorm_bwd_quant_dual on h."""
-    _want(x, torch.bfloat16, 2, "x")
+    _want(x, _BF16, 2, "x")
     M, H = shape = x.shape
-    _exact(res, shape, torch.bfloat16, "res")
-    _exact(h, shape, torch.bfloat16, "h")
-    _exact_dense(gamma, (H,), torch.bfloat16, "gamma")
-    _exact_dense(q, shape, torch.uint8, "q")
-    _scales_1x128(s, _groups(H), M, "s"); _dense(s, "s")
+    # one comparison of everything on the way of a correct call; the checks one by one (and
+    # their messages) only where it fails
+    if not (isinstance(res, _T) and isinstance(h, _T) and isinstance(gamma, _T)
+            and isinstance(q, _T) and res.dtype == h.dtype == gamma.dtype == _BF16
+            and q.dtype == _U8 and res.shape == h.shape == q.shape == shape and gamma.shape == (H,)
+            and gamma.is_contiguous() and q.is_contiguous()):
+        _exact(res, shape, _BF16, "res")
+        _exact(h, shape, _BF16, "h")
+        _exact_dense(gamma, (H,), _BF16, "gamma")
+        _exact_dense(q, shape, _U8, "q")
+    lds = _scales_dense(s, _groups(H), M, "s")
     px, pr, pg, ph, pq, ps = _pointers((x, "x"), (res, "res"), (gamma, "gamma"), (h, "h"),
                                        (q, "q"), (s, "s"))
     _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, x, px, pr, pg, M, H,
-         _row_stride(x, M, H, "x"), _row_stride(res, M, H, "res"), eps, ph, _row_stride(h, M, H, "h"), pq, ps,
-         s.shape[1])
+         _row_stride(x, M, H, "x"), _row_stride(res, M, H, "res"), eps, ph,
+         _row_stride(h, M, H, "h"), pq, ps, lds)
 
 
 def add_rmsnorm_quant_alloc(x, res, gamma, eps, stream=None):
@@ -690,12 +705,12 @@ def _grouped_weight(qw, sw, offsets, name, N_at):
 
 
 def _grouped_rows(q, s, width, name_q, name_s):
-    """Row operand q [M,width] with its 1x128 scales; returns M."""
-    _want(q, torch.uint8, 2, name_q)
-    M = q.shape[0]
-    _exact_dense(q, (M, width), torch.uint8, name_q)
-    _scales_1x128(s, _groups(width), M, name_s); _dense(s, name_s)
-    return M
+    """Row operand q [M,width] with its 1x128 scales; returns M and the scales' lds."""
+    _want(q, _U8, 2, name_q)
+    M, cols = q.shape
+    if cols != width or not q.is_contiguous():
+        _exact_dense(q, (M, width), _U8, name_q)
+    return M, _scales_dense(s, _groups(width), M, name_s)
 
 
 def grouped_linear_fwd(qa, sa, qw, sw, offsets, y, stream=None):
@@ -703,35 +718,36 @@ def grouped_linear_fwd(qa, sa, qw, sw, offsets, y, stream=None):
     times qw[e] ([E,N,K], see grouped_quant_weight_alloc) -> the same rows of y BF16 [M,N].
     Rows of no expert are left as they are. offsets: int32 [E+1] on the device."""
     E, N, K = _grouped_weight(qw, sw, offsets, "qw", 1)
-    M = _grouped_rows(qa, sa, K, "qa", "sa")
+    M, lds = _grouped_rows(qa, sa, K, "qa", "sa")
     _exact(y, (M, N), torch.bfloat16, "y")
     pa, psa, pw, psw, po, py = _pointers((qa, "qa"), (sa, "sa"), (qw, "qw"), (sw, "sw"),
                                          (offsets, "offsets"), (y, "y"))
     _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, qa, pa, psa,
-         sa.shape[1], pw, psw, po, E, M, N, K, py, _row_stride(y, M, N, "y"))
+         lds, pw, psw, po, E, M, N, K, py, _row_stride(y, M, N, "y"))
 
 
 def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
     """linear_dgrad with one weight per expert: qdy [M,N] x W[e] -> dx BF16 [M,K] (weights
     transposed and stacked, qwT [K,E,N]). Rows of no expert are left as they are."""
     E, N, K = _grouped_weight(qwT, sw, offsets, "qwT", 2)
-    M = _grouped_rows(qdy, sdy, N, "qdy", "sdy")
+    M, lds = _grouped_rows(qdy, sdy, N, "qdy", "sdy")
     _exact(dx, (M, K), torch.bfloat16, "dx")
     pa, psa, pw, psw, po, px = _pointers((qdy, "qdy"), (sdy, "sdy"), (qwT, "qwT"), (sw, "sw"),
                                          (offsets, "offsets"), (dx, "dx"))
     _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, qdy, pa, psa,
-         sdy.shape[1], pw, psw, po, E, M, N, K, px, _row_stride(dx, M, K, "dx"))
+         lds, pw, psw, po, E, M, N, K, px, _row_stride(dx, M, K, "dx"))
 
 
 def _grouped_columns(qT, sT, rows, name_q, name_s):
     """Transposed codes [rows,P] with their 128x1 scales [P/128,rows]; returns P."""
-    _want(qT, torch.uint8, 2, name_q)
-    P = qT.shape[1]
+    _want(qT, _U8, 2, name_q)
+    n, P = qT.shape
     if P % 128:
         raise ValueError("%s must have a multiple of 128 columns, got %s" % (
             name_q, tuple(qT.shape)))
-    _exact_dense(qT, (rows, P), torch.uint8, name_q)
-    _exact_dense(sT, (P // 128, rows), torch.float32, name_s)
+    if n != rows or not qT.is_contiguous():
+        _exact_dense(qT, (rows, P), _U8, name_q)
+    _exact_dense(sT, (P // 128, rows), _F32, name_s)
     return P
 
 
@@ -746,9 +762,8 @@ def grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, strea
     if (q_row is None) != (s_row is None):
         raise ValueError("q_row and s_row must be given together")
     if q_row is not None:
-        _exact_dense(q_row, shape, torch.uint8, "q_row")
-        _scales_1x128(s_row, _groups(N), M, "s_row"); _dense(s_row, "s_row")
-        lds_row = s_row.shape[1]
+        _exact_dense(q_row, shape, _U8, "q_row")
+        lds_row = _scales_dense(s_row, _groups(N), M, "s_row")
     P = _grouped_columns(q_colT, s_col, N, "q_colT", "s_col")
     pd, po, pq, ps, pqT, psT = _pointers((dy, "dy"), (offsets, "offsets"), (q_row, "q_row"),
                                          (s_row, "s_row"), (q_colT, "q_colT"), (s_col, "s_col"))
@@ -775,12 +790,12 @@ def grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream=None):
     _want(q, torch.uint8, 2, "q")
     E = _offsets(offsets)
     K = q.shape[1]
-    M = _grouped_rows(q, s, K, "q", "s")
+    M, lds = _grouped_rows(q, s, K, "q", "s")
     P = _grouped_columns(qT, sT, K, "qT", "sT")
     pq, ps, po, pqT, psT = _pointers((q, "q"), (s, "s"), (offsets, "offsets"), (qT, "qT"),
                                      (sT, "sT"))
     _run(_lib.fp8q_grouped_transpose_quant_fp8, "fp8q_grouped_transpose_quant_fp8", stream, q,
-         pq, ps, po, E, M, K, s.shape[1], pqT, psT, P)
+         pq, ps, po, E, M, K, lds, pqT, psT, P)
 
 
 def grouped_transpose_quant_fp8_alloc(q, s, offsets, stream=None):

@@ -94,7 +94,7 @@ struct GroupedGemm {
 // Average rows per expert up to which the forward and DGrad run as strips of weight rows
 // (at 64 rows 252 against 297 us on the large-tile kernel, at 128 rows 375 against 297: see
 // launch_grouped_strips).
-constexpr int64_t kStripMaxRows = 96;
+constexpr int64_t kStripMaxRows = 72;
 
 fp8q_status launch_grouped_strips(const GroupedGemm& g, cudaStream_t stream);
 

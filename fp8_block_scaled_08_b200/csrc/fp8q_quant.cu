@@ -2065,9 +2065,15 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
   int2* const stage_rows = reinterpret_cast<int2*>(abort_flag + 2);
   int* const goff = reinterpret_cast<int*>(stage_rows + kStages);
   int* const gfirst = goff + grp.experts + 1;
-  if constexpr (kGrouped)
+  if constexpr (kGrouped) {
+    if (threadIdx.x == kA6Threads - 1) {  // the copies' descriptors, while the offsets come
+      prefetch_tensormap(&tmD);
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmQT);
+    }
     group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
                      groups_of_rows);
+  }
   __syncthreads();
   const int64_t NB = (N + 127) >> 7;
   const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * NB;
@@ -2123,6 +2129,12 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         if (lane == 0) mbar_arrive(empty + b);
         continue;
       }
+      const int2 rows = kGrouped ? stage_rows[b] : make_int2(0, 0);
+      if (kGrouped && rows.y <= warp * 16) {  // none of this warp's rows
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + b);
+        continue;
+      }
       const int64_t mb = t / NB, nb = t - mb * NB;
       const int roff = (warp * 16 + rl) * 128 + hh * 64;
       uint16_t* row = reinterpret_cast<uint16_t*>(base + b * kStageBytes) + roff;
@@ -2145,7 +2157,6 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4*>(row + ((j + lane) & 7) * 8);
       }
-      const int2 rows = kGrouped ? stage_rows[b] : make_int2(0, 0);
       const float amax = half_row_amax(w);
       __syncwarp();  // every lane's reads of the tile are complete (their values are used)
       if (lane == 0) mbar_arrive(empty + b);
@@ -2199,20 +2210,20 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         break;
       const uint32_t* tw = reinterpret_cast<const uint32_t*>(base + b * kStageBytes) + q4 * 32 * 64 + (c0 >> 1);
       uint32_t w[32];  // columns c0, c0 + 1 of rows 32 q4 + k
+      uint32_t m0 = 0u, m1 = 0u;
+      const int valid = kGrouped ? stage_rows[b].y - q4 * 32 : 32;  // rows of this quarter
+      if (!kGrouped || valid > 0) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) w[k] = tw[k * 64];
-      if constexpr (kGrouped) {  // rows past the group's end
-        const int valid = stage_rows[b].y - q4 * 32;
-        if (valid < 32) {
+        for (int k = 0; k < 32; ++k) w[k] = tw[k * 64];
+        if (kGrouped && valid < 32) {  // rows past the group's end
 #pragma unroll
           for (int k = 0; k < 32; ++k) w[k] = k < valid ? w[k] : 0u;
         }
-      }
-      uint32_t m0 = 0u, m1 = 0u;
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        m0 = bf16x2_maxabs_xs(m0, w[k]);
-        m1 = bf16x2_maxabs_xs(m1, w[k + 1]);
+        for (int k = 0; k < 32; k += 2) {
+          m0 = bf16x2_maxabs_xs(m0, w[k]);
+          m1 = bf16x2_maxabs_xs(m1, w[k + 1]);
+        }
       }
       __syncwarp();  // every lane's reads of the tile are complete (their values are used)
       if (lane == 0) mbar_arrive(empty + b);
@@ -2228,10 +2239,14 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
       if (q4 == 0 && nb * 128 + c0 < N)
         *reinterpret_cast<float2*>(s_col + mb * N + nb * 128 + c0) = make_float2(g0.s, g1.s);
       uint32_t o0[8], o1[8];
-      if (__any_sync(kFull, g0.small || g1.small))
+      if (kGrouped && valid <= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o0[k] = o1[k] = 0u;
+      } else if (__any_sync(kFull, g0.small || g1.small)) {
         col_codes<true, 32>(w, g0, g1, o0, o1);
-      else
+      } else {
         col_codes<false, 32>(w, g0, g1, o0, o1);
+      }
       // staging row c holds column c's 128 codes; 16-byte chunk k of the row (rows 16k ..
       // 16k+15 of the tile) sits at position k ^ (c & 7) (the 128-byte swizzle)
 #pragma unroll
@@ -3032,6 +3047,11 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x == kRqThreads - 1) {  // the copies' descriptors, while the offsets come
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmS);
+    prefetch_tensormap(&tmQT);
+  }
   group_table_fill(off, first, grp.offsets, grp.experts, static_cast<int>(M), err, groups_of_rows);
   __syncthreads();
   const int64_t KB = (K + 127) >> 7;
@@ -3104,12 +3124,16 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
     }
     float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float xa[4], xb[4];
-      dequant4(w[2 * j], rsc[8 * j], xa);
-      dequant4(w[2 * j + 1], rsc[8 * j + 1], xb);
+    for (int j4 = 0; j4 < 4; ++j4) {
+      if (32 * j4 >= rr.y) break;  // no rows from here on
 #pragma unroll
-      for (int c = 0; c < 4; ++c) m[c] = fmaxf(fmaxf(m[c], fabsf(xa[c])), fabsf(xb[c]));
+      for (int j = 4 * j4; j < 4 * j4 + 4; ++j) {
+        float xa[4], xb[4];
+        dequant4(w[2 * j], rsc[8 * j], xa);
+        dequant4(w[2 * j + 1], rsc[8 * j + 1], xb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m[c] = fmaxf(fmaxf(m[c], fabsf(xa[c])), fabsf(xb[c]));
+      }
     }
     GroupScale g[4];
 #pragma unroll
@@ -3133,9 +3157,10 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
       for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(w[j]));
 #pragma unroll
       for (int j2 = 0; j2 < 8; ++j2) {
-        uint32_t o[4];
+        uint32_t o[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
+          if (32 * (j2 >> 1) >= rr.y) break;  // no rows from here on
           const int j = 2 * j2 + jj;
           uint32_t ca = requant4(w[2 * j], rsc[8 * j], g);
           uint32_t cb = requant4(w[2 * j + 1], rsc[8 * j + 1], g);
