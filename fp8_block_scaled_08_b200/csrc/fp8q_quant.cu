@@ -1192,15 +1192,17 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1) rmsnorm_lane_kernel(
 // ---------------------------------------------------------------------------
 constexpr int kTileElems = 128 * 128;
 
-// Arguments of a grouped tile kernel: the experts' row offsets (fp8q_grouped.cuh), the
-// length of a row of the transposed codes, and the row codes' address (the rows of a group
-// that ends inside a warp's box are stored one by one). Unused by the ungrouped kernels.
+// Arguments of a grouped tile kernel: the experts' row offsets (fp8q_grouped.cuh) and
+// the row codes' address (the rows of a group that ends inside a warp's box are stored one by
+// one).
 struct TileGroups {
   const int32_t* offsets;
   int experts;
-  int64_t P;
   uint8_t* q_row;
 };
+
+// Units of a grouped call: 128-row groups per expert (128x1 groups restart at each expert).
+__device__ __forceinline__ int groups_of_rows(int lo, int hi) { return (hi - lo + 127) >> 7; }
 
 struct TileSmem {
   uint8_t* buf[2];
@@ -2019,18 +2021,12 @@ __device__ __forceinline__ void half_row_codes(const uint4 (&w)[8], const GroupS
   }
 }
 
-// Units of a grouped call: 128-row groups per expert (128x1 groups restart at each expert).
-__device__ __forceinline__ int groups_of_rows(int lo, int hi) { return (hi - lo + 127) >> 7; }
-
-// kGrouped: the 128-row blocks are the experts' groups; a group's last rows may belong to
-// the next expert: they count as zeros in the columns, and their row codes are not stored
-// here (they are rows of that expert's own groups).
-template <class Src, bool kRows, bool kGrouped = false>
+template <class Src, bool kRows>
 __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmD1,
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQT, Src src,
     int64_t M, int64_t N, float* __restrict__ s_row, int64_t lds_row, float* __restrict__ s_col,
-    unsigned* err, uint64_t limit_ns, const TileGroups grp) {
+    unsigned* err, uint64_t limit_ns) {
   using L = A6Layout<Src>;
   constexpr int kStages = L::kStages;
   constexpr uint32_t kStageBytes = L::kStageBytes;
@@ -2059,24 +2055,9 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
     *abort_flag = 0;
     fence_barrier_init();
   }
-  // grouped: first row and number of rows of the tile in each stage, written by the
-  // producer before it arrives on the stage's barrier (a search of the table by each of the
-  // sixteen consumer warps measured 71 us against 60 for 16384 x 4096)
-  int2* const stage_rows = reinterpret_cast<int2*>(abort_flag + 2);
-  int* const goff = reinterpret_cast<int*>(stage_rows + kStages);
-  int* const gfirst = goff + grp.experts + 1;
-  if constexpr (kGrouped) {
-    if (threadIdx.x == kA6Threads - 1) {  // the copies' descriptors, while the offsets come
-      prefetch_tensormap(&tmD);
-      prefetch_tensormap(&tmQ);
-      prefetch_tensormap(&tmQT);
-    }
-    group_table_fill(goff, gfirst, grp.offsets, grp.experts, static_cast<int>(M), err,
-                     groups_of_rows);
-  }
   __syncthreads();
   const int64_t NB = (N + 127) >> 7;
-  const int64_t tiles = (kGrouped ? gfirst[grp.experts] : (M + 127) >> 7) * NB;
+  const int64_t tiles = ((M + 127) >> 7) * NB;
   if (warp == 16) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -2088,15 +2069,9 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         const uint32_t ph = static_cast<uint32_t>(i / kStages) & 1u;
         if (i >= kStages && !mbar_wait(empty + b, ph ^ 1u, ctl)) { ok = false; break; }
         const int64_t mb = t / NB, nb = t - mb * NB;
-        int64_t r0 = mb * 128;
-        if constexpr (kGrouped) {
-          const int e = group_find(gfirst, grp.experts, static_cast<int>(mb));
-          r0 = goff[e] + 128 * (mb - gfirst[e]);
-          stage_rows[b] = make_int2(static_cast<int>(r0), min(128, goff[e + 1] - static_cast<int>(r0)));
-        }
         mbar_arrive_expect_tx(full + b, kStageBytes);
         tma_load_2d(base + b * kStageBytes, &tmD, static_cast<int32_t>(nb * 128),
-                    static_cast<int32_t>(r0), full + b);
+                    static_cast<int32_t>(mb * 128), full + b);
         if (Src::kBoxes == 2)
           tma_load_2d(base + b * kStageBytes + kA6Tile, &tmD1, static_cast<int32_t>(nb * 128),
                       static_cast<int32_t>(mb * 128), full + b);
@@ -2126,12 +2101,6 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
       const int b = i % kStages;
       if (!mbar_wait_warp(full + b, static_cast<uint32_t>(i / kStages) & 1u, ctl)) break;
       if (!kRows && !Src::kForm) {
-        if (lane == 0) mbar_arrive(empty + b);
-        continue;
-      }
-      const int2 rows = kGrouped ? stage_rows[b] : make_int2(0, 0);
-      if (kGrouped && rows.y <= warp * 16) {  // none of this warp's rows
-        __syncwarp();
         if (lane == 0) mbar_arrive(empty + b);
         continue;
       }
@@ -2167,25 +2136,15 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         __syncwarp();
       }
       half_row_codes(w, g, out + rl * 128 + hh * 64, lane);
-      const int64_t m0 = (kGrouped ? rows.x : mb * 128) + warp * 16;
-      const int64_t r1 = kGrouped ? rows.x + rows.y : M;  // one past the tile's rows
-      if (!kGrouped || m0 + 16 <= r1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&tmQ, out, static_cast<int32_t>(nb * 128), static_cast<int32_t>(m0));
-          tma_store_commit();
-        }
-        stored = true;
-      } else if (m0 + rl < r1) {  // the group ends inside this box: row by row
-        const int64_t col = nb * 128 + hh * 64;
-        const uint4* src_row = reinterpret_cast<const uint4*>(out + rl * 128 + hh * 64);
-        uint4* dst = reinterpret_cast<uint4*>(grp.q_row + (m0 + rl) * N + col);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (col + 16 * j < N) dst[j] = src_row[j];  // N is a multiple of 16
+      fence_proxy_async_smem();
+      __syncwarp();
+      const int64_t m0 = mb * 128 + warp * 16;
+      if (lane == 0) {
+        tma_store_2d(&tmQ, out, static_cast<int32_t>(nb * 128), static_cast<int32_t>(m0));
+        tma_store_commit();
       }
-      if (hh == 0 && m0 + rl < r1) s_row[nb * lds_row + m0 + rl] = g.s;
+      stored = true;
+      if (hh == 0 && m0 + rl < M) s_row[nb * lds_row + m0 + rl] = g.s;
     }
   } else {
     // ------------------------------------------------------------ 128x1 columns
@@ -2210,20 +2169,13 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
         break;
       const uint32_t* tw = reinterpret_cast<const uint32_t*>(base + b * kStageBytes) + q4 * 32 * 64 + (c0 >> 1);
       uint32_t w[32];  // columns c0, c0 + 1 of rows 32 q4 + k
+#pragma unroll
+      for (int k = 0; k < 32; ++k) w[k] = tw[k * 64];
       uint32_t m0 = 0u, m1 = 0u;
-      const int valid = kGrouped ? stage_rows[b].y - q4 * 32 : 32;  // rows of this quarter
-      if (!kGrouped || valid > 0) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) w[k] = tw[k * 64];
-        if (kGrouped && valid < 32) {  // rows past the group's end
-#pragma unroll
-          for (int k = 0; k < 32; ++k) w[k] = k < valid ? w[k] : 0u;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          m0 = bf16x2_maxabs_xs(m0, w[k]);
-          m1 = bf16x2_maxabs_xs(m1, w[k + 1]);
-        }
+      for (int k = 0; k < 32; k += 2) {
+        m0 = bf16x2_maxabs_xs(m0, w[k]);
+        m1 = bf16x2_maxabs_xs(m1, w[k + 1]);
       }
       __syncwarp();  // every lane's reads of the tile are complete (their values are used)
       if (lane == 0) mbar_arrive(empty + b);
@@ -2239,14 +2191,10 @@ __global__ void __launch_bounds__(kA6Threads, 1) a6_tile_kernel(
       if (q4 == 0 && nb * 128 + c0 < N)
         *reinterpret_cast<float2*>(s_col + mb * N + nb * 128 + c0) = make_float2(g0.s, g1.s);
       uint32_t o0[8], o1[8];
-      if (kGrouped && valid <= 0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o0[k] = o1[k] = 0u;
-      } else if (__any_sync(kFull, g0.small || g1.small)) {
+      if (__any_sync(kFull, g0.small || g1.small))
         col_codes<true, 32>(w, g0, g1, o0, o1);
-      } else {
+      else
         col_codes<false, 32>(w, g0, g1, o0, o1);
-      }
       // staging row c holds column c's 128 codes; 16-byte chunk k of the row (rows 16k ..
       // 16k+15 of the tile) sits at position k ^ (c & 7) (the 128-byte swizzle)
 #pragma unroll
@@ -2978,17 +2926,27 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float s, const GroupSca
   return cvt_e4m3x4(t[0], t[1], t[2], t[3]) | (w & 0x80808080u);
 }
 
-// 8 rows x 32 columns of codes: ca and cb hold columns 4c .. 4c + 3 of rows 2g and 2g + 1
-// (lane 8g + c); o0 and o1 become rows 0-3 and 4-7 of column 4c + g.
+// 8 rows x 32 columns of codes: ca and cb hold columns 4c .. 4c + 3 of the two rows of
+// row pair p(g) (lane 8g + c); o0 and o1 become rows 0-3 and 4-7 of column 4c + g. The row
+// pairs are p(g) = g (rows 2g, 2g + 1) or, kCrossed, 0, 2, 1, 3 for g = 0 .. 3.
+template <bool kCrossed>
 struct RowsToColumns {
   uint32_t keep, send, sel0, sel1;
   bool upper;
   __device__ __forceinline__ explicit RowsToColumns(int gr) {
     keep = (gr & 1) ? 0x7632u : 0x5410u;
     send = keep ^ 0x2222u;
-    sel0 = gr == 0 ? 0x5410u : gr == 1 ? 0x1054u : gr == 2 ? 0x7632u : 0x3276u;
-    sel1 = sel0 ^ 0x2222u;
     upper = gr & 2;
+    // after the two exchanges `mine` holds the pairs of g and g ^ 2, `other` those of g ^ 1
+    // and g ^ 3
+    if (kCrossed) {
+      const uint32_t swap = upper ? 0x2222u : 0u;
+      sel0 = ((gr & 1) ? 0x7654u : 0x3210u) ^ swap;
+      sel1 = ((gr & 1) ? 0x3210u : 0x7654u) ^ swap;
+    } else {
+      sel0 = gr == 0 ? 0x5410u : gr == 1 ? 0x1054u : gr == 2 ? 0x7632u : 0x3276u;
+      sel1 = sel0 ^ 0x2222u;
+    }
   }
   __device__ __forceinline__ void operator()(uint32_t ca, uint32_t cb, uint32_t& o0,
                                              uint32_t& o1) const {
@@ -3007,7 +2965,7 @@ struct RowsToColumns {
 __device__ __noinline__ void requant_tile_div(const uint8_t* worda, const uint8_t* wordb,
                                               const float* rsc, float4 gs, int rows, int gr,
                                               uint8_t* orow, int col) {
-  const RowsToColumns to_columns(gr);
+  const RowsToColumns<false> to_columns(gr);
 #pragma unroll 1
   for (int j = 0; j < 16; ++j) {
     uint32_t c[2], o[2];
@@ -3091,7 +3049,7 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
   }
   // -------------------------------------------------------------- consumers
   const int grp4 = warp >> 2, gr = lane >> 3, cw = lane & 7;
-  const RowsToColumns to_columns(gr);
+  const RowsToColumns<false> to_columns(gr);
   // this lane's column after the transpose, and its row of the warp's staging tile (128-byte
   // swizzle: the 16-byte writes of a warp take 4 wavefronts, the least possible)
   const int col = 4 * cw + gr;
@@ -3185,6 +3143,296 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
     }
   }
   if (lane == 0) tma_store_wait_all();
+}
+
+// a6 for a grouped call. The 128-row blocks are the experts' groups (rows past a group's end
+// count as zeros in the columns and their row codes are left to the expert they belong to);
+// a tile arrives as two boxes of 64 columns with the 128-byte swizzle. Five warpgroups:
+//   0      warp 0 is the producer (four stages); the others hand their registers on.
+//   1, 2   1x128 rows, eight warps, every tile: lane l of warp w holds half of row
+//          16w + l % 16 (one box row; the halves meet by one shuffle); its chunks j sit at
+//          positions j ^ (row % 8), so the reads and the 16-byte writes of the codes into
+//          the swizzled staging box are free of bank conflicts.
+//   3, 4   128x1 columns, alternate tiles (a group of four warps owns two stages), each
+//          warp 32 columns over all 128 rows as in grouped_requant_kernel: no barrier
+//          between warps; lane 8g + c holds columns 4c .. 4c + 3 of two rows of every eight,
+//          rows 0, 4, 2, 6 and the next one for g = 0 .. 3 (which with the swizzle puts the
+//          two g of a half-warp's 8-byte reads into different halves of the row).
+// 60.7 us (4.5 TB/s) at 16384 x 4096 over 8 experts, 10.6 us at 301 x 3584 over 16; the
+// dense kernel's layout (eight column warps that meet twice a tile) took 60.7 and 11.7. The
+// tile copies alone take 29.7, with the rows 40.5, with the columns 45.0: both passes are
+// bound by their instructions (about 15 per element in all), not by the memory.
+constexpr int kGgStages = 4;
+constexpr int kGgThreads = 640;
+constexpr uint32_t kGgRegsRow = 88, kGgRegsCol = 136, kGgRegsRest = 24;
+static_assert(128 * (kGgRegsRest + 2 * kGgRegsRow + 2 * kGgRegsCol) <= 96 * kGgThreads,
+              "register hand-over exceeds the launch allocation");
+constexpr uint32_t kGgBox = 128 * 64 * 2;
+constexpr uint32_t kGgTile = 2 * kGgBox;
+constexpr uint32_t kGgOffCol = kGgStages * kGgTile;         // 8 x [32 columns][128 codes]
+constexpr uint32_t kGgOffRow = kGgOffCol + 8 * 32 * 128;    // 8 x [16 rows][128 codes]
+constexpr uint32_t kGgOffTab = kGgOffRow + 8 * 16 * 128;    // scale and reciprocal tables
+constexpr uint32_t kGgOffRows = kGgOffTab + 256 * 4;        // int2 per stage
+constexpr uint32_t kGgOffBar = kGgOffRows + kGgStages * 8;
+constexpr uint32_t kGgOffOffsets = kGgOffBar + 2 * kGgStages * 8 + 16;
+constexpr size_t grouped_grad_smem(int E) { return 1024 + kGgOffOffsets + group_table_bytes(E); }
+static_assert(grouped_grad_smem(kMaxExperts) <= 232448, "shared memory budget of one sm_100 CTA");
+
+// Four codes of a row: two packed BF16 pairs with the scales of their columns.
+template <bool kDiv>
+__device__ __forceinline__ uint32_t codes4_cols(uint2 w, const GroupScale (&g)[4]) {
+  const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+  float t[4];
+  if (kDiv) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) t[c] = g[c].small ? __fdiv_rn(x[c], g[c].s) : quot(x[c], g[c]);
+  } else {
+    quot2(x[0], x[1], g[0], g[1], t[0], t[1]);
+    quot2(x[2], x[3], g[2], g[3], t[2], t[3]);
+  }
+  return cvt_e4m3x4(t[0], t[1], t[2], t[3]);
+}
+
+// A column warp's tile where some column has a tiny scale (divides): rolled up and out of
+// line, away from the registers of the usual path.
+__device__ __noinline__ void grad_tile_div(const uint8_t* worda, const uint8_t* wordb,
+                                           const float* amax, int rows, int gr, int row0,
+                                           uint8_t* orow, int col) {
+  const RowsToColumns<true> to_columns(gr);
+  GroupScale g[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    g[c] = group_scale(amax[c]);
+    g[c].small = true;
+  }
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j) {
+    uint2 wa = *reinterpret_cast<const uint2*>(worda + j * 1024);
+    uint2 wb = *reinterpret_cast<const uint2*>(wordb + j * 1024);
+    if (8 * j + row0 >= rows) wa = make_uint2(0u, 0u);
+    if (8 * j + row0 + 1 >= rows) wb = make_uint2(0u, 0u);
+    uint32_t o0, o1;
+    to_columns(codes4_cols<true>(wa, g), codes4_cols<true>(wb, g), o0, o1);
+    *reinterpret_cast<uint2*>(orow + (((j >> 1) ^ (col & 7)) << 4) + 8 * (j & 1)) = make_uint2(o0, o1);
+  }
+}
+
+template <bool kRows>
+__global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
+    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmQ,
+    const __grid_constant__ CUtensorMap tmQT, int64_t M, int64_t N, float* __restrict__ s_row,
+    int64_t lds_row, float* __restrict__ s_col, unsigned* err, uint64_t limit_ns,
+    const TileGroups grp) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* tab = reinterpret_cast<float*>(base + kGgOffTab);
+  int2* stage_rows = reinterpret_cast<int2*>(base + kGgOffRows);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + kGgOffBar);
+  uint64_t* empty = full + kGgStages;
+  int* abort_flag = reinterpret_cast<int*>(empty + kGgStages);
+  int* off = reinterpret_cast<int*>(base + kGgOffOffsets);
+  int* first = off + grp.experts + 1;
+  const WaitCtl ctl{abort_flag, err, limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x >= 128 && threadIdx.x < 256) {
+    tab[threadIdx.x - 128] = kScaleMant[threadIdx.x - 128];
+    tab[threadIdx.x] = kRecipMant[threadIdx.x - 128];
+  }
+  if (threadIdx.x == kGgThreads - 1) {  // the copies' descriptors, while the offsets come
+    prefetch_tensormap(&tmD);
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmQT);
+  }
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < kGgStages; ++b) {
+      mbar_init(full + b, 1);
+      mbar_init(empty + b, (kRows ? 8 : 0) + 4);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  group_table_fill(off, first, grp.offsets, grp.experts, static_cast<int>(M), err, groups_of_rows);
+  __syncthreads();
+  const int64_t NB = (N + 127) >> 7;
+  const int64_t tiles = first[grp.experts] * NB;
+  if (warp < 4) {
+    regs_decrease<kGgRegsRest>();
+    // ------------------------------------------------------------ producer
+    if (warp == 0 && lane == 0) {
+      uint32_t issued = 0, par = 0;
+      bool ok = true;
+      int i = 0;
+      for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+        const int b = i % kGgStages;
+        const uint32_t ph = static_cast<uint32_t>(i / kGgStages) & 1u;
+        const int mb = static_cast<int>(t / NB), nb = static_cast<int>(t - mb * NB);
+        const int e = group_find(first, grp.experts, mb);
+        const int r0 = off[e] + 128 * (mb - first[e]);
+        if (i >= kGgStages && !mbar_wait(empty + b, ph ^ 1u, ctl)) { ok = false; break; }
+        stage_rows[b] = make_int2(r0, min(128, off[e + 1] - r0));
+        mbar_arrive_expect_tx(full + b, kGgTile);
+        tma_load_2d(base + b * kGgTile, &tmD, nb * 128, r0, full + b);
+        tma_load_2d(base + b * kGgTile + kGgBox, &tmD, nb * 128 + 64, r0, full + b);
+        issued |= 1u << b;
+        par = (par & ~(1u << b)) | (ph << b);
+      }
+      if (!ok) {  // let every copy already issued land before the CTA exits
+        for (int b = 0; b < kGgStages; ++b) {
+          if (!((issued >> b) & 1u)) continue;
+          const uint32_t a = smem_u32(full + b);
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try_wait(a, (par >> b) & 1u))
+            if (global_timer_ns() - t0 > limit_ns) break;
+        }
+      }
+    }
+  } else if (warp < 12) {
+    regs_decrease<kGgRegsRow>();
+    // ------------------------------------------------------------ 1x128 rows
+    if (kRows) {
+      const int rw = warp - 4, rl = lane & 15, hh = lane >> 4;
+      uint8_t* out = base + kGgOffRow + rw * (16 * 128);
+      bool stored = false;
+      int i = 0;
+      for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+        const int b = i % kGgStages;
+        if (!mbar_wait_warp(full + b, static_cast<uint32_t>(i / kGgStages) & 1u, ctl)) break;
+        const int2 rows = stage_rows[b];
+        if (rows.y <= rw * 16) {  // none of this warp's rows
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty + b);
+          continue;
+        }
+        const uint8_t* row = base + b * kGgTile + hh * kGgBox + (rw * 16 + rl) * 128;
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (rl & 7)) << 4));
+        const float amax = half_row_amax(w);
+        __syncwarp();  // every lane's reads of the tile are complete (their values are used)
+        if (lane == 0) mbar_arrive(empty + b);
+        const GroupScale g = group_scale_bf16_sm(amax, tab);
+        const bool small = __any_sync(kFull, g.small);
+        const int64_t mb = t / NB, nb = t - mb * NB;
+        const int m0 = rows.x + rw * 16;
+        const bool whole = rw * 16 + 16 <= rows.y;
+        if (stored) {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+        }
+        const int64_t c0 = nb * 128 + hh * 64;
+        uint8_t* dst = grp.q_row + static_cast<int64_t>(m0 + rl) * N + c0;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint2 c = small ? codes8_words<true>(w[j], g) : codes8_words<false>(w[j], g);
+          const uint2 d = small ? codes8_words<true>(w[j + 1], g) : codes8_words<false>(w[j + 1], g);
+          const uint4 v = make_uint4(c.x, c.y, d.x, d.y);
+          if (whole)
+            *reinterpret_cast<uint4*>(out + rl * 128 + (((4 * hh + (j >> 1)) ^ (rl & 7)) << 4)) = v;
+          else if (rw * 16 + rl < rows.y && c0 + 8 * j < N)  // the group ends inside the box
+            *reinterpret_cast<uint4*>(dst + 8 * j) = v;      // (N is a multiple of 16)
+        }
+        if (whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmQ, out, static_cast<int32_t>(nb * 128), m0);
+            tma_store_commit();
+          }
+          stored = true;
+        }
+        if (hh == 0 && rw * 16 + rl < rows.y) s_row[nb * lds_row + m0 + rl] = g.s;
+      }
+      if (stored && lane == 0) tma_store_wait_all();
+    }
+  } else {
+    regs_increase<kGgRegsCol>();
+    // ------------------------------------------------------------ 128x1 columns
+    const int cg = (warp - 12) >> 2, cw = warp & 3;  // group, 32 columns of the tile
+    const int gr = lane >> 3, c8 = lane & 7;
+    const int x0 = 4 * (gr & 1) + (gr & 2);          // first row of this lane in every eight
+    const int chunk = 4 * (cw & 1) + (c8 >> 1);
+    const uint32_t boff = (cw >> 1) * kGgBox + 8 * (c8 & 1);
+    const uint32_t offa = boff + x0 * 128 + ((chunk ^ x0) << 4);
+    const uint32_t offb = boff + (x0 + 1) * 128 + ((chunk ^ (x0 + 1)) << 4);
+    const RowsToColumns<true> to_columns(gr);
+    const int col = 4 * c8 + gr;  // this lane's column after the transpose
+    uint8_t* out = base + kGgOffCol + (warp - 12) * (32 * 128);
+    uint8_t* orow = out + col * 128;
+    int i = cg;
+    for (int64_t t = blockIdx.x + static_cast<int64_t>(cg) * gridDim.x; t < tiles;
+         t += 2 * static_cast<int64_t>(gridDim.x), i += 2) {
+      const int b = i % kGgStages;
+      if (!mbar_wait_warp(full + b, static_cast<uint32_t>(i / kGgStages) & 1u, ctl)) break;
+      const int rows = stage_rows[b].y;
+      const uint8_t* tile = base + b * kGgTile;
+      uint2 w[32];
+      uint32_t m0 = 0u, m1 = 0u;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        w[2 * j] = *reinterpret_cast<const uint2*>(tile + offa + j * 1024);
+        w[2 * j + 1] = *reinterpret_cast<const uint2*>(tile + offb + j * 1024);
+      }
+      if (rows < 128) {  // past the group's end: rows of the next expert, or of nobody
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (8 * j + x0 >= rows) w[2 * j] = make_uint2(0u, 0u);
+          if (8 * j + x0 + 1 >= rows) w[2 * j + 1] = make_uint2(0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        m0 = bf16x2_maxabs_xs(m0, w[j].x);
+        m1 = bf16x2_maxabs_xs(m1, w[j].y);
+      }
+#pragma unroll
+      for (int d = 8; d <= 16; d <<= 1) {
+        m0 = bf16x2_maxabs_xs(m0, __shfl_xor_sync(kFull, m0, d));
+        m1 = bf16x2_maxabs_xs(m1, __shfl_xor_sync(kFull, m1, d));
+      }
+      const float amax[4] = {fabsf(bf16_lo(m0)), fabsf(bf16_hi(m0)), fabsf(bf16_lo(m1)),
+                             fabsf(bf16_hi(m1))};
+      GroupScale g[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) g[c] = group_scale_bf16_sm(amax[c], tab);
+      const int64_t mb = t / NB, nb = t - mb * NB;
+      const int64_t c0 = nb * 128 + 32 * cw;
+      if (gr == 0 && c0 + 4 * c8 < N)  // N is a multiple of 16: the four are in or out
+        *reinterpret_cast<float4*>(s_col + mb * N + c0 + 4 * c8) =
+            make_float4(g[0].s, g[1].s, g[2].s, g[3].s);
+      if (lane == 0) tma_store_wait_read();  // the previous tile's codes have left
+      __syncwarp();
+      if (__any_sync(kFull, g[0].small || g[1].small || g[2].small || g[3].small)) {
+        grad_tile_div(tile + offa, tile + offb, amax, rows, gr, x0, orow, col);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + b);
+      } else {
+        __syncwarp();  // every lane's reads of the tile are complete (their values are used)
+        if (lane == 0) mbar_arrive(empty + b);
+#pragma unroll
+        for (int j2 = 0; j2 < 8; ++j2) {
+          uint32_t o[4] = {0u, 0u, 0u, 0u};
+          if (16 * j2 < rows) {
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              const int j = 2 * j2 + jj;
+              to_columns(codes4_cols<false>(w[2 * j], g), codes4_cols<false>(w[2 * j + 1], g),
+                         o[2 * jj], o[2 * jj + 1]);
+            }
+          }
+          *reinterpret_cast<uint4*>(orow + ((j2 ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && c0 < N) {  // the copy clips a ragged N
+        tma_store_2d(&tmQT, out, static_cast<int32_t>(mb * 128), static_cast<int32_t>(c0));
+        tma_store_commit();
+      }
+    }
+    if (lane == 0) tma_store_wait_all();
+  }
 }
 
 // a2 on a tile ring. The block scale is shared by a block and its transpose, so qT is the
@@ -3620,14 +3868,12 @@ extern "C" fp8q_status fp8q_transpose_quant_bf16(const uint16_t* dy, int64_t M, 
     static std::atomic<int> occ[64];
     const int per_sm = resident_ctas(a6_tile_kernel<TileGrad, true>, kA6Threads, kSmem, occ);
     a6_tile_kernel<TileGrad, true><<<grid_for(tiles, per_sm), kA6Threads, kSmem, st>>>(
-        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs,
-        TileGroups{});
+        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs);
   } else {
     static std::atomic<int> occ[64];
     const int per_sm = resident_ctas(a6_tile_kernel<TileGrad, false>, kA6Threads, kSmem, occ);
     a6_tile_kernel<TileGrad, false><<<grid_for(tiles, per_sm), kA6Threads, kSmem, st>>>(
-        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs,
-        TileGroups{});
+        tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row, lds_row, s_col, err, kWaitLimitNs);
   }
   return launch_status("transpose_quant_bf16 launch");
 }
@@ -3694,8 +3940,7 @@ extern "C" fp8q_status fp8q_rmsnorm_quant_dual(const uint16_t* x, const uint16_t
   static std::atomic<int> occ[64];
   const int per_sm = resident_ctas(kern, kA6Threads, kSmem, occ);
   kern<<<grid_for((M / 128) * (H / 128), per_sm), kA6Threads, kSmem, st>>>(
-      tmx, tmx, tmq, tmqt, TileRms{rstd, gamma}, M, H, s_row, lds_row, s_col, err, kWaitLimitNs,
-      TileGroups{});
+      tmx, tmx, tmq, tmqt, TileRms{rstd, gamma}, M, H, s_row, lds_row, s_col, err, kWaitLimitNs);
   return launch_status("rmsnorm_quant_dual launch");
 }
 
@@ -3881,6 +4126,26 @@ extern "C" fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t*
   return launch_status("add_rmsnorm_quant launch");
 }
 
+// Opts the grouped gradient quantizer in to its shared memory and checks that the launch
+// allocation covers its register hand-over (a build below it would wait for good).
+template <class Kernel>
+static bool grouped_grad_setup(Kernel k, std::atomic<int>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (done[dev].load(std::memory_order_acquire)) return true;
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, k);
+  if (e != cudaSuccess || attr.maxThreadsPerBlock < kGgThreads ||
+      static_cast<uint32_t>(attr.numRegs) * kGgThreads <
+          128 * (kGgRegsRest + 2 * kGgRegsRow + 2 * kGgRegsCol)) {
+    set_last_error("grouped gradient quantizer register budget",
+                   e != cudaSuccess ? e : cudaErrorLaunchOutOfResources);
+    cudaGetLastError();
+    return false;
+  }
+  return allow_max_smem(k, done);
+}
+
 extern "C" fp8q_status fp8q_grouped_transpose_quant_bf16(
     const uint16_t* dy, const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t lddy,
     uint8_t* q_row, float* s_row, int64_t lds_row, uint8_t* q_colT, float* s_col, int64_t P,
@@ -3897,27 +4162,26 @@ extern "C" fp8q_status fp8q_grouped_transpose_quant_bf16(
     return FP8Q_ERR_ALIGN;
   if (!sm100_sm_count()) return FP8Q_ERR_UNSUPPORTED;
   CUtensorMap tmd, tmq, tmqt;
-  if (!encode_tmap_2d(&tmd, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, N, M, lddy * 2, 128, 128,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_tmap_2d(&tmqt, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_colT, P, N, P, 128, 128,
+  if (!encode_tmap_2d(&tmd, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, N, M, lddy * 2, 64, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_2d(&tmqt, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_colT, P, N, P, 128, 32,
                       CU_TENSOR_MAP_SWIZZLE_128B))
     return FP8Q_ERR_UNSUPPORTED;
   if (q_row && !encode_tmap_2d(&tmq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_row, N, M, N, 128, 16,
-                               CU_TENSOR_MAP_SWIZZLE_NONE))
+                               CU_TENSOR_MAP_SWIZZLE_128B))
     return FP8Q_ERR_UNSUPPORTED;
   if (!q_row) tmq = tmqt;  // unused
   unsigned* err = device_error_word();
   if (!err) return FP8Q_ERR_CUDA;
   const int64_t tiles = grouped_padded_rows(M, E) / 128 * ((N + 127) / 128);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t smem = a6_smem<TileGrad>() + 8 * A6Layout<TileGrad>::kStages +
-                      group_table_bytes(static_cast<int>(E));
-  const TileGroups grp{offsets, static_cast<int>(E), P, q_row};
-  auto kern = q_row ? a6_tile_kernel<TileGrad, true, true> : a6_tile_kernel<TileGrad, false, true>;
+  const TileGroups grp{offsets, static_cast<int>(E), q_row};
+  const size_t smem = grouped_grad_smem(static_cast<int>(E));
+  auto kern = q_row ? grouped_grad_kernel<true> : grouped_grad_kernel<false>;
   static std::atomic<int> smem_ok[2][64];
-  if (!allow_max_smem(kern, smem_ok[q_row ? 1 : 0])) return FP8Q_ERR_CUDA;
-  kern<<<grid_for(tiles, 1), kA6Threads, smem, st>>>(tmd, tmd, tmq, tmqt, TileGrad{}, M, N, s_row,
-                                                     lds_row, s_col, err, kWaitLimitNs, grp);
+  if (!grouped_grad_setup(kern, smem_ok[q_row ? 1 : 0])) return FP8Q_ERR_CUDA;
+  kern<<<grid_for(tiles, 1), kGgThreads, smem, st>>>(tmd, tmq, tmqt, M, N, s_row, lds_row, s_col,
+                                                     err, kWaitLimitNs, grp);
   return launch_status("grouped_transpose_quant_bf16 launch");
 }
 
@@ -3949,7 +4213,7 @@ extern "C" fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const 
   const int64_t tiles = grouped_padded_rows(M, E) / 128 * KB;
   static std::atomic<int> smem_ok[64];
   if (!allow_max_smem(grouped_requant_kernel, smem_ok)) return FP8Q_ERR_CUDA;
-  const TileGroups grp{offsets, static_cast<int>(E), P, nullptr};
+  const TileGroups grp{offsets, static_cast<int>(E), nullptr};
   grouped_requant_kernel<<<grid_for(tiles, 1), kRqThreads, requant_smem(static_cast<int>(E)),
                            static_cast<cudaStream_t>(stream)>>>(tmq, tms, tmqt, M, K, sT, err,
                                                                 kWaitLimitNs, grp);
