@@ -832,9 +832,7 @@ fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
   const int64_t mblocks = kCol ? (g.Mg + kPairM - 1) / kPairM
                                : (g.rows + (kPairM + 2) * std::min(g.E, g.rows)) / kPairM;
   const int64_t tiles = mblocks * nblocks * (kCol ? g.E : 1);
-  if (tiles > 0x7FFFFFFF || out_rows > 0x7FFFFFFF || g.b_inner > 0x7FFFFFFF ||
-      g.b_outer > 0x7FFFFFFF || a_inner > 0x7FFFFFFF)
-    return FP8Q_ERR_SHAPE;
+  if (tiles > 0x7FFFFFFF || out_rows > 0x7FFFFFFF || !g.extents_ok()) return FP8Q_ERR_SHAPE;
   CUtensorMap tmA, tmB, tmSA, tmSB, tmY;
   bool ok = encode_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.A, a_inner, a_rows, a_inner, BK,
                            BM, CU_TENSOR_MAP_SWIZZLE_128B) &&
@@ -881,11 +879,12 @@ fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
   return launch_status("grouped gemm_kernel launch");
 }
 
-// Forward or DGrad: up to kStripMaxRows rows per expert on average (of the rows the arrays
-// hold; the routing itself is known on the device only) take the strip kernel.
+// Forward or DGrad: strips of weight rows where that is faster, else the pair kernel.
 fp8q_status launch_grouped_rows(const GroupedGemm& g, cudaStream_t stream) {
-  if (g.out_extents_ok() && g.rows <= kStripMaxRows * g.E) return launch_grouped_strips(g, stream);
-  return launch_grouped<false>(g, stream);
+  if (!g.extents_ok()) return FP8Q_ERR_SHAPE;
+  bool taken = false;
+  const fp8q_status st = launch_grouped_strips(g, taken, stream);
+  return taken ? st : launch_grouped<false>(g, stream);
 }
 
 }  // namespace

@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
 }
 
 template <int kNT>
-fp8q_status launch_strips(const GroupedGemm& g, int sms, cudaStream_t stream) {
+fp8q_status launch_strips(const GroupedGemm& g, int64_t token_tiles, int sms,
+                          cudaStream_t stream) {
   using S = GmShape<kNT>;
   const int64_t KB = g.Kg / kGmBK;
   const uint32_t fixed = 1024 + S::kFixed + group_table_bytes(static_cast<int>(g.E));
@@ -369,11 +370,12 @@ fp8q_status launch_strips(const GroupedGemm& g, int sms, cudaStream_t stream) {
   p.stages = static_cast<int32_t>(
       std::min<uint32_t>(kGmMaxStages, (kGmMaxSmem - fixed) / S::kStage));
   const size_t smem = fixed + static_cast<size_t>(p.stages) * S::kStage;
-  // Strip height: 128 rows fill the MMA; where even one tile for every expert that can have
-  // rows leaves half of the SMs without one, lower strips (the rest of the MMA's rows is
-  // whatever the stage holds, its lanes are never read) put more SMs on the weights.
+  // Strip height: 128 rows fill the MMA; where its tiles would leave half of the SMs without
+  // one, lower strips (the rest of the MMA's rows is whatever the stage holds, its lanes are
+  // never read) put more SMs on the weights (8 experts of 512 x 2048, 2 rows each: 14.3 us
+  // with 128 rows, 12.4 with 32).
   p.height = kGmRows;
-  while (p.height > 32 && std::min(g.E, g.rows) * (g.Ng / p.height) * 2 <= sms) p.height /= 2;
+  while (p.height > 32 && token_tiles * (g.Ng / p.height) * 2 <= sms) p.height /= 2;
   CUtensorMap tmW, tmX, tmSA;
   const uint64_t wdims[3] = {kGmBK, static_cast<uint64_t>(g.b_outer),
                              static_cast<uint64_t>(g.b_inner / kGmBK)};
@@ -429,21 +431,40 @@ fp8q_status launch_strips(const GroupedGemm& g, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-fp8q_status launch_grouped_strips(const GroupedGemm& g, cudaStream_t stream) {
+// The choice goes by the sizes alone (the routing itself is known on the device only); every
+// kernel takes every routing and gives the same bits. Measured, one B200, L2 flushed, us:
+//
+// 1. Where one tile per SM holds the whole product, its time is the serial walk over the
+//    slices, about 0.33 / 0.37 / 0.53 us a slice with tiles of 32 / 64 / 128 token rows and
+//    0.63 on the large-tile kernel: the narrowest tile that fits. One expert of 512 x 5120:
+//    300 rows 20.5 with 64-row tiles, 26.6 with 128, 30.8 large; one of 4096 x 4096, 100
+//    rows: 24.6 with 128, 26.6 large. An expert's rows are taken as one and a half times the
+//    average (experts over the tile's width double its tiles).
+// 2. Otherwise few rows per expert are bound by the weights (strips), many by the tensor
+//    cores (large tiles). Forward, 64 experts of 4096 x 4096, at 8 / 16 / 32 / 64 / 128 rows
+//    per expert: 32-row tiles 184 / 184 / 205 / 320 / 562, 64-row 182 / 182 / 192 / 234 / 375,
+//    128-row 246 / 248 / 250 / 252 / 377, large 277 / 281 / 289 / 297 / 297; DGrad, 16 experts
+//    of 3584 x 1024, at 16 / 32 / 64 / 128 rows: 22.6 / 28.7 / 32.8 / 41.0, 22.6 / 22.6 / 30.7
+//    / 36.9, 24.6 / 26.6 / 26.6 / 41.0, large 28.7 / 30.7 / 30.7 / 30.7. 184 us are 5.9 TB/s of
+//    weights, 0.91 of the measured copy rate. (Promoting one slice per TMEM buffer instead
+//    of two took 198 / 239 us at 16 / 32 rows. The 128-row tiles are bound by the promotion.)
+fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_t stream) {
+  taken = true;
   const int sms = sm100_sm_count();
   if (!sms) return FP8Q_ERR_UNSUPPORTED;
-  // Token rows of a tile, by the average rows of an expert. Measured, one B200, L2 flushed
-  // (us; in brackets the large-tile kernel): forward, 64 experts of 4096 x 4096, at 8 / 16 /
-  // 32 / 64 / 128 rows: 32-row tiles 184 / 184 / 205 / 320 / 562, 64-row tiles 182 / 182 /
-  // 192 / 234 / 375, 128-row tiles 246 / 248 / 250 / 252 / 377 (277 / 281 / 289 / 297 /
-  // 297); DGrad, 16 experts of 3584 x 1024, at 16 / 32 / 64 / 128 rows: 22.6 / 28.7 / 32.8 /
-  // 41.0, 22.6 / 22.6 / 30.7 / 36.9, 24.6 / 26.6 / 26.6 / 41.0 (28.7 / 30.7 / 30.7 / 30.7);
-  // forward, one expert of 4096 x 4096, 1 row: 16.4 with 32-row tiles, 20.5 with 64-row ones.
-  // 184 us are 5.9 TB/s of weights, 0.91 of the measured copy rate. Promoting one slice per
-  // TMEM buffer instead of two took 198 / 239 us at 16 / 32 rows (32- / 64-row tiles).
-  if (g.rows <= 16 * g.E) return launch_strips<32>(g, sms, stream);
-  if (g.rows <= 48 * g.E) return launch_strips<64>(g, sms, stream);
-  return launch_strips<128>(g, sms, stream);
+  const int64_t used = std::min(g.E, g.rows);  // experts that can have rows
+  const int64_t avg = (g.rows + used - 1) / used;
+  const int64_t likely = used == 1 ? avg : avg + avg / 2;
+  auto token_tiles = [&](int64_t nt) { return used * ((likely + 3 + nt - 1) / nt); };
+  const int64_t strips = g.Ng / kGmRows;
+  if (token_tiles(32) * strips <= sms) return launch_strips<32>(g, token_tiles(32), sms, stream);
+  if (token_tiles(64) * strips <= sms) return launch_strips<64>(g, token_tiles(64), sms, stream);
+  if (token_tiles(128) * strips <= sms) return launch_strips<128>(g, token_tiles(128), sms, stream);
+  if (g.rows <= 16 * g.E) return launch_strips<32>(g, token_tiles(32), sms, stream);
+  if (g.rows <= 48 * g.E) return launch_strips<64>(g, token_tiles(64), sms, stream);
+  if (g.rows <= 72 * g.E) return launch_strips<128>(g, token_tiles(128), sms, stream);
+  taken = false;
+  return FP8Q_OK;
 }
 
 }  // namespace fp8q

@@ -86,16 +86,14 @@ struct GroupedGemm {
   void* y;
   int64_t ldy;
   // every extent is a tensor-copy coordinate
-  bool out_extents_ok() const {
-    return rows <= 0x7FFFFFFF && b_inner <= 0x7FFFFFFF && b_outer <= 0x7FFFFFFF && Kg <= 0x7FFFFFFF;
+  bool extents_ok() const {
+    return rows <= 0x7FFFFFFF && Ng <= 0x7FFFFFFF && Kg <= 0x7FFFFFFF && b_inner <= 0x7FFFFFFF &&
+           b_outer <= 0x7FFFFFFF;
   }
 };
 
-// Average rows per expert up to which the forward and DGrad run as strips of weight rows
-// (at 64 rows 252 against 297 us on the large-tile kernel, at 128 rows 375 against 297: see
-// launch_grouped_strips).
-constexpr int64_t kStripMaxRows = 72;
-
-fp8q_status launch_grouped_strips(const GroupedGemm& g, cudaStream_t stream);
+// The forward or DGrad as strips of weight rows; `taken` is false (nothing launched) where
+// the large-tile kernel is the better one for these sizes.
+fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_t stream);
 
 }  // namespace fp8q
