@@ -21,11 +21,13 @@
 //    brings kG * 128 bytes of each of the weight rows, another the token rows of the same
 //    slices (single-slice stages measured 1-4 % slower: twice the copies and barriers).
 //  * Warp 0 is the producer; warps 1 and 2 issue the MMAs of alternate stages into up to 8
-//    TMEM buffers of kG slices; the other warps promote a buffer at a time (figures at
+//    TMEM buffers of kG slices; warp 3 multiplies each slice's token scales by its block
+//    scale, in shared memory; the other warps promote a buffer at a time (figures at
 //    launch_grouped_strips): lane l of warp w holds weight row 32 * (w % 4) + l and the
 //    accumulators of the tile's tokens (of half of them, in two warpgroups, from 64 tokens
-//    on; four warpgroups measured up to 19 % slower); a slice's token scales are read from
-//    shared memory as broadcasts and multiplied by the block scale.
+//    on; four warpgroups measured up to 19 % slower) and reads the scale products as
+//    broadcasts (with the products formed by every promoting thread 64- and 128-row tiles
+//    took 2-10 % longer).
 //  * Epilogue: two lanes exchange halves so that each stores two neighbouring outputs of
 //    one token (a warp store writes two runs of 64 bytes).
 //
@@ -45,7 +47,8 @@ namespace fp8q {
 namespace {
 
 constexpr int kGmIssuers = 2;    // warps 1 and 2
-constexpr int kGmPromote = 3;    // first promotion warp
+constexpr int kGmScaleWarp = 3;  // forms the scale products
+constexpr int kGmPromote = 4;    // first promotion warp
 constexpr int kGmRows = 128;     // weight rows of a tile
 constexpr int kGmBK = 128;
 constexpr int kGmMaxStages = 8;
@@ -64,10 +67,10 @@ struct GmShape {
   static constexpr uint32_t kXBytes = kG * kNT * kGmBK;
   static constexpr uint32_t kStage = kWBytes + kXBytes;
   static constexpr uint32_t kSlot = kG * kNT * 4;  // a multiple of 128
-  static constexpr uint32_t kBars = 2 * kGmMaxStages + 2 * kBufs + 2 * kGmScRing + 1;
+  static constexpr uint32_t kBars = 2 * kGmMaxStages + 2 * kBufs + 3 * kGmScRing + 1;
   static constexpr uint32_t kFixed = kGmScRing * kSlot + kBars * 8 + 16;
   static_assert(kBufs % kGmIssuers == 0, "an accumulator buffer is always the same issuer's");
-  static_assert(kNT % 16 == 0 && kNT <= 256 && kSlot % 128 == 0, "MMA N and copy alignment");
+  static_assert(kNT % 32 == 0 && kNT <= 256 && kSlot % 128 == 0, "MMA N and copy alignment");
   static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512,
                 "TMEM allocations are powers of two");
 };
@@ -145,7 +148,8 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
   uint64_t* tempty = tfull + kBufs;
   uint64_t* sfull = tempty + kBufs;
   uint64_t* sempty = sfull + kGmScRing;
-  uint64_t* done = sempty + kGmScRing;
+  uint64_t* pfull = sempty + kGmScRing;  // scale products of a slot
+  uint64_t* done = pfull + kGmScRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* off = reinterpret_cast<int*>(tmem_slot + 4);
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
     }
     for (int i = 0; i < kGmScRing; ++i) {
       mbar_init(sfull + i, 1);
+      mbar_init(pfull + i, 1);
       mbar_init(sempty + i, (p.height >> 5) * S::kHalves);
     }
     mbar_init(done, kGmIssuers);
@@ -259,6 +264,37 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
       gm_wait_drain(done, 0, p.wait_limit_ns);
     }
     __syncwarp();
+  } else if (warp == kGmScaleWarp) {
+    // ------------------------------------------------------------ scale products
+    // Each slot's row scales times the slice's block scale, in place: one product per token
+    // and slice instead of one per token, slice and promoting thread (as many packed
+    // multiplications there as the promotion has FMAs).
+    uint32_t si = 0, sph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      const GmTile g = gm_tile<kNT>(t, p, off, first);
+      const float* sbp = p.sb + g.e * p.sb_se + ((g.strip * p.height) >> 7) * p.sb_sj;
+      // 32 slices at a time: lane l holds slice 32 * (kb / 32) + l; the next ones 16 ahead
+      auto sb_fetch = [&](int kk) -> float { return kk < KB ? __ldg(sbp + kk * p.sb_sr) : 0.0f; };
+      float sbv = sb_fetch(lane), sbx = 0.0f;
+      for (int kb = 0; kb < KB; kb += kG) {
+        if ((kb & 31) == 16) sbx = sb_fetch(kb + 16 + lane);
+        if ((kb & 31) == 0 && kb > 0) sbv = sbx;
+        if (!mbar_wait_warp(sfull + si, sph, ctl)) { ok = false; break; }
+        float* sc = reinterpret_cast<float*>(slots + si * S::kSlot);
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
+          const float sb = __shfl_sync(0xFFFFFFFFu, sbv, (kb + j) & 31);
+#pragma unroll
+          for (int i = 0; i < kNT; i += 32)
+            sc[j * kNT + i + lane] = __fmul_rn(sc[j * kNT + i + lane], sb);
+        }
+        fence_proxy_async_smem();  // before a later copy into this slot
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull + si);
+        if (++si == kGmScRing) { si = 0; sph ^= 1u; }
+      }
+    }
   } else {
     // ------------------------------------------------------------ promotion + epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
@@ -269,30 +305,13 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
     const int col0 = ((warp - kGmPromote) >> 2) * kCols;  // this warpgroup's tokens
     uint32_t it = 0, si = 0, sph = 0;
     bool ok = true;
-    // block scales, 32 slices at a time: lane l holds slice 32 * (kb / 32) + l
-    auto sb_fetch = [&](const GmTile& g, int kk) -> float {
-      return kk < KB ? __ldg(p.sb + g.e * p.sb_se + ((g.strip * p.height) >> 7) * p.sb_sj +
-                                kk * p.sb_sr) : 0.0f;
-    };
-    GmTile g{};
-    float sbv = 0.0f;
-    if (static_cast<int>(blockIdx.x) < my_tiles) {
-      g = gm_tile<kNT>(blockIdx.x, p, off, first);
-      sbv = sb_fetch(g, lane);
-    }
     for (int t = blockIdx.x; ok && t < my_tiles; t += gridDim.x) {
       float acc[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-      float sbx = 0.0f;
       for (int k = 0; k < nst; ++k) {
         const int kb = k * kG;
-        if ((kb & 31) == 16) sbx = sb_fetch(g, kb + 16 + lane);
-        if ((kb & 31) == 0 && kb > 0) sbv = sbx;
-        float sb[kG];
-#pragma unroll
-        for (int j = 0; j < kG; ++j) sb[j] = __shfl_sync(0xFFFFFFFFu, sbv, (kb + j) & 31);
-        if (!mbar_wait_warp(sfull + si, sph, ctl)) { ok = false; break; }
+        if (!mbar_wait_warp(pfull + si, sph, ctl)) { ok = false; break; }
         const float4* sa = reinterpret_cast<const float4*>(slots + si * S::kSlot) + col0 / 4;
         const uint32_t buf = it % kBufs, tph = (it / kBufs) & 1u;
         if (!mbar_wait_warp(tfull + buf, tph, ctl)) { ok = false; break; }
@@ -312,12 +331,10 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
 #pragma unroll
               for (int i = 0; i < kChunk; i += 4) {
                 const float4 s4 = sa[(j * kNT + c + i) / 4];  // broadcast
-                float s0, s1, s2, s3;
-                mul2(s0, s1, s4.x, s4.y, sb[j], sb[j]);
-                mul2(s2, s3, s4.z, s4.w, sb[j], sb[j]);
                 float* a = acc + c + i;
-                fma2(a[0], a[1], __uint_as_float(r[j][i]), __uint_as_float(r[j][i + 1]), s0, s1);
-                fma2(a[2], a[3], __uint_as_float(r[j][i + 2]), __uint_as_float(r[j][i + 3]), s2, s3);
+                fma2(a[0], a[1], __uint_as_float(r[j][i]), __uint_as_float(r[j][i + 1]), s4.x, s4.y);
+                fma2(a[2], a[3], __uint_as_float(r[j][i + 2]), __uint_as_float(r[j][i + 3]), s4.z,
+                     s4.w);
               }
             }
           }
@@ -332,11 +349,7 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
         if (++si == kGmScRing) { si = 0; sph ^= 1u; }
       }
       if (!ok) break;
-      const GmTile o = g;
-      if (t + static_cast<int>(gridDim.x) < my_tiles) {  // the next tile's scales meanwhile
-        g = gm_tile<kNT>(t + gridDim.x, p, off, first);
-        sbv = sb_fetch(g, lane);
-      }
+      const GmTile o = gm_tile<kNT>(t, p, off, first);
       // lanes 2i and 2i + 1 exchange: the even lane stores both outputs of token j, the odd
       // lane those of token j + 1
       const int odd = lane & 1;
