@@ -448,19 +448,19 @@ fp8q_status launch_strips(const GroupedGemm& g, int64_t token_tiles, int sms,
 // kernel takes every routing and gives the same bits. Measured, one B200, L2 flushed, us:
 //
 // 1. Where one tile per SM holds the whole product, its time is the serial walk over the
-//    slices, about 0.33 / 0.37 / 0.53 us a slice with tiles of 32 / 64 / 128 token rows and
-//    0.63 on the large-tile kernel: the narrowest tile that fits. One expert of 512 x 5120:
-//    300 rows 20.5 with 64-row tiles, 26.6 with 128, 30.8 large; one of 4096 x 4096, 100
-//    rows: 24.6 with 128, 26.6 large. An expert's rows are taken as one and a half times the
-//    average (experts over the tile's width double its tiles).
+//    slices: the narrowest tile that fits. One expert of 4096 x 4096, 1 row: 16.4 / 18.5 /
+//    24.6 with tiles of 32 / 64 / 128 token rows, 26.6 with large tiles; 512 x 5120, 300
+//    rows: 18.5 / 18.4 / 24.6, large 30.7; DGrad, 16 experts of 3584 x 1024, at 16 / 32 / 64
+//    rows each: 22.6 / 28.7 / 32.8, 22.5 / 24.6 / 30.7, 24.6 / 26.6 / 26.6, large 28.7 / 30.7 /
+//    30.8. An expert's rows are taken as one and a half times the average (an expert over
+//    the tile's width needs a second tile).
 // 2. Otherwise few rows per expert are bound by the weights (strips), many by the tensor
 //    cores (large tiles). Forward, 64 experts of 4096 x 4096, at 8 / 16 / 32 / 64 / 128 rows
-//    per expert: 32-row tiles 184 / 184 / 205 / 320 / 562, 64-row 182 / 182 / 192 / 234 / 375,
-//    128-row 246 / 248 / 250 / 252 / 377, large 277 / 281 / 289 / 297 / 297; DGrad, 16 experts
-//    of 3584 x 1024, at 16 / 32 / 64 / 128 rows: 22.6 / 28.7 / 32.8 / 41.0, 22.6 / 22.6 / 30.7
-//    / 36.9, 24.6 / 26.6 / 26.6 / 41.0, large 28.7 / 30.7 / 30.7 / 30.7. 184 us are 5.9 TB/s of
-//    weights, 0.91 of the measured copy rate. (Promoting one slice per TMEM buffer instead
-//    of two took 198 / 239 us at 16 / 32 rows. The 128-row tiles are bound by the promotion.)
+//    each: 32-row tiles 186 / 186 / 199 / 293 / 510, 64-row 182 / 184 / 193 / 221 / 342, 128-row
+//    238 / 240 / 244 / 248 / 389 (bound by the promotion), large 281 / 289 / 293 / 301 / 309.
+//    Back to back, under the power cap, 2 rows each take 171 with 32-row tiles (6.3 TB/s of
+//    weights, 0.97 of the measured copy rate) and 197 with 64-row tiles.
+//    (Promoting one slice per TMEM buffer instead of two took 198 / 239 at 16 / 32 rows.)
 fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_t stream) {
   taken = true;
   const int sms = sm100_sm_count();
@@ -474,8 +474,7 @@ fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_
   if (token_tiles(64) * strips <= sms) return launch_strips<64>(g, token_tiles(64), sms, stream);
   if (token_tiles(128) * strips <= sms) return launch_strips<128>(g, token_tiles(128), sms, stream);
   if (g.rows <= 16 * g.E) return launch_strips<32>(g, token_tiles(32), sms, stream);
-  if (g.rows <= 48 * g.E) return launch_strips<64>(g, token_tiles(64), sms, stream);
-  if (g.rows <= 72 * g.E) return launch_strips<128>(g, token_tiles(128), sms, stream);
+  if (g.rows <= 96 * g.E) return launch_strips<64>(g, token_tiles(64), sms, stream);
   taken = false;
   return FP8Q_OK;
 }
