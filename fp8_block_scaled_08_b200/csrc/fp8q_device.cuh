@@ -124,6 +124,20 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
 }
 
 // ---------------------------------------------------------------------------
+// Launches that overlap the end of the kernel before them (launch_overlapped): such a
+// kernel reads and writes nothing in global memory before wait_for_previous_kernel, which
+// every thread passes; it lets its successor start its own preparations with
+// let_next_kernel_start (a successor waits in turn for this kernel to be complete, so the
+// order of all memory operations is that of the stream).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // TMA (tiled tensor loads, no multicast). The shared-memory destination (or source of
 // a store) must start on a 128-byte boundary (1024 with the 128-byte swizzle), and the
 // innermost coordinate times the element size must be a multiple of 16 bytes.

@@ -307,7 +307,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmY);
     if (kColScaleB) prefetch_tensormap(&tmSB);
   }
+  if (warp == 1) tmem_alloc_pair<kTmemCols>(tmem_slot);
   if constexpr (kGrouped) {
+    let_next_kernel_start();
+    wait_for_previous_kernel();
     int* off = reinterpret_cast<int*>(smem + kSmemUsed);
     group_table_fill(off, off + p.experts + 1, p.offsets, p.experts,
                      kColScaleB ? 0x7FFFFFFF - BK : p.limit, p.err,
@@ -318,7 +321,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       atomicOr(p.err, kErrOffsets);
     __syncwarp();
   }
-  if (warp == 1) tmem_alloc_pair<kTmemCols>(tmem_slot);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -874,9 +876,8 @@ fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
   p.wait_limit_ns = kWaitLimitNs;
   if (!p.err) return FP8Q_ERR_CUDA;
   const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, max_pairs));
-  gemm_kernel<kCol, false, true>
-      <<<grid, kThreads, kGroupedSmemBytes, stream>>>(tmA, tmB, tmSA, tmSB, tmY, p);
-  return launch_status("grouped gemm_kernel launch");
+  return launch_overlapped("grouped gemm_kernel launch", gemm_kernel<kCol, false, true>, grid,
+                           kThreads, kGroupedSmemBytes, stream, tmA, tmB, tmSA, tmSB, tmY, p);
 }
 
 // Forward or DGrad: strips of weight rows where that is faster, else the pair kernel.

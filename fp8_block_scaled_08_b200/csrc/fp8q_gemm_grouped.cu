@@ -178,8 +178,10 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmSA);
   }
-  group_table_fill(off, first, p.offsets, p.experts, p.rows, p.err, gm_token_tiles<kNT>);
+  let_next_kernel_start();
   if (warp == 1) tmem_alloc<S::kTmemCols>(tmem_slot);
+  wait_for_previous_kernel();
+  group_table_fill(off, first, p.offsets, p.experts, p.rows, p.err, gm_token_tiles<kNT>);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -437,9 +439,9 @@ fp8q_status launch_strips(const GroupedGemm& g, int64_t token_tiles, int sms,
     }
     smem_ok[dev].store(1, std::memory_order_release);
   }
-  grouped_strip_kernel<kNT><<<static_cast<int>(std::min<int64_t>(tiles, sms)), S::kThreads, smem,
-                              stream>>>(tmW, tmX, tmSA, p);
-  return launch_status("grouped_strip_kernel launch");
+  return launch_overlapped("grouped_strip_kernel launch", grouped_strip_kernel<kNT>,
+                           static_cast<int>(std::min<int64_t>(tiles, sms)), S::kThreads, smem, stream,
+                           tmW, tmX, tmSA, p);
 }
 
 }  // namespace

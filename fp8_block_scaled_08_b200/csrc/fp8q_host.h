@@ -43,6 +43,29 @@ inline fp8q_status launch_status(const char* where = "launch") {
   return FP8Q_ERR_CUDA;
 }
 
+// Launches a kernel that passes wait_for_previous_kernel before it touches global memory:
+// its CTAs may become resident, set their barriers up and fetch their descriptors while the
+// kernel before it on the stream ends.
+template <class... Params, class... Args>
+fp8q_status launch_overlapped(const char* where, void (*kernel)(Params...), int grid, int threads,
+                              size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  if (e == cudaSuccess) return FP8Q_OK;
+  set_last_error(where, e);
+  cudaGetLastError();
+  return FP8Q_ERR_CUDA;
+}
+
 // Bounded waits inside the kernels give up after this long (nanoseconds).
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 

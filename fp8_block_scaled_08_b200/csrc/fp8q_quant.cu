@@ -940,6 +940,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) add_rmsnorm_quant_kernel(
   const int lane = tid & 31, wid = tid >> 5;
   const int nch = static_cast<int>(H >> 3);
   int flip = 0;  // the shared words alternate, so a row needs no barrier behind it
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   uint4 nx[kChunks], nr[kChunks], gm[kChunks];  // the row to come, and gamma
   auto load = [&](int64_t m) {
 #pragma unroll
@@ -3010,6 +3012,8 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
     prefetch_tensormap(&tmS);
     prefetch_tensormap(&tmQT);
   }
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   group_table_fill(off, first, grp.offsets, grp.experts, static_cast<int>(M), err, groups_of_rows);
   __syncthreads();
   const int64_t KB = (K + 127) >> 7;
@@ -3252,6 +3256,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
     *abort_flag = 0;
     fence_barrier_init();
   }
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   group_table_fill(off, first, grp.offsets, grp.experts, static_cast<int>(M), err, groups_of_rows);
   __syncthreads();
   const int64_t NB = (N + 127) >> 7;
@@ -4121,9 +4127,8 @@ extern "C" fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t*
                                     : Choice{add_rmsnorm_quant_kernel<512, 4, true, 1>, 512, 1};
   const Choice k = many ? many_k : few_k;
   const int64_t grid = many ? std::min<int64_t>(M, static_cast<int64_t>(sms) * k.ctas) : M;
-  k.kern<<<static_cast<int>(grid), k.threads, 0, st>>>(x, res, gamma, M, H, ldx, ldres, eps, h, ldh,
-                                                       q, s, lds);
-  return launch_status("add_rmsnorm_quant launch");
+  return launch_overlapped("add_rmsnorm_quant launch", k.kern, static_cast<int>(grid), k.threads, 0,
+                           st, x, res, gamma, M, H, ldx, ldres, eps, h, ldh, q, s, lds);
 }
 
 // Opts the grouped gradient quantizer in to its shared memory and checks that the launch
@@ -4180,9 +4185,9 @@ extern "C" fp8q_status fp8q_grouped_transpose_quant_bf16(
   auto kern = q_row ? grouped_grad_kernel<true> : grouped_grad_kernel<false>;
   static std::atomic<int> smem_ok[2][64];
   if (!grouped_grad_setup(kern, smem_ok[q_row ? 1 : 0])) return FP8Q_ERR_CUDA;
-  kern<<<grid_for(tiles, 1), kGgThreads, smem, st>>>(tmd, tmq, tmqt, M, N, s_row, lds_row, s_col,
-                                                     err, kWaitLimitNs, grp);
-  return launch_status("grouped_transpose_quant_bf16 launch");
+  return launch_overlapped("grouped_transpose_quant_bf16 launch", kern, grid_for(tiles, 1),
+                           kGgThreads, smem, st, tmd, tmq, tmqt, M, N, s_row, lds_row, s_col, err,
+                           kWaitLimitNs, grp);
 }
 
 extern "C" fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const float* s,
@@ -4214,8 +4219,8 @@ extern "C" fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const 
   static std::atomic<int> smem_ok[64];
   if (!allow_max_smem(grouped_requant_kernel, smem_ok)) return FP8Q_ERR_CUDA;
   const TileGroups grp{offsets, static_cast<int>(E), nullptr};
-  grouped_requant_kernel<<<grid_for(tiles, 1), kRqThreads, requant_smem(static_cast<int>(E)),
-                           static_cast<cudaStream_t>(stream)>>>(tmq, tms, tmqt, M, K, sT, err,
-                                                                kWaitLimitNs, grp);
-  return launch_status("grouped_transpose_quant_fp8 launch");
+  return launch_overlapped("grouped_transpose_quant_fp8 launch", grouped_requant_kernel,
+                           grid_for(tiles, 1), kRqThreads, requant_smem(static_cast<int>(E)),
+                           static_cast<cudaStream_t>(stream), tmq, tms, tmqt, M, K, sT, err,
+                           kWaitLimitNs, grp);
 }

@@ -651,6 +651,72 @@ def test_offsets_out_of_order_are_clamped_and_reported(fq, bad):
     assert fq.device_error() == fq.FP8Q_OK
 
 
+def test_most_experts(fq):
+    """1024 experts (the table's limit), most of them without rows, against the same rows in
+    a call with only the experts that have some."""
+    E, N, K = 1024, 128, 256
+    counts = np.zeros(E, np.int64)
+    counts[[0, 3, 31, 32, 500, 1022, 1023]] = [2, 1, 140, 5, 33, 1, 7]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    M, used = int(off[-1]), np.flatnonzero(counts)
+    o = dev_offsets(off)
+    o_used = dev_offsets(np.concatenate([[0], np.cumsum(counts[used])]).astype(np.int32))
+    qw, sw, qwT = weights(fq, E, N, K, 3170)
+    qw1, sw1 = qw[used].contiguous(), sw[used].contiguous()
+    qwT1 = qwT[:, used].contiguous()
+    x = workloads.activations_bf16((M, K), 0, 3171, DEV)
+    dy = workloads.gradients_bf16((M, N), 1e-3, 0, 3172, DEV)
+
+    def run(qw, sw, qwT, o):
+        qa, sa = fq.quant_act_1x128_alloc(x)
+        y, dx = torch.zeros_like(dy), torch.zeros_like(x)
+        fq.grouped_linear_fwd(qa, sa, qw, sw, o, y)
+        qr, sr, qc, sc = fq.grouped_transpose_quant_bf16_alloc(dy, o)
+        fq.grouped_linear_dgrad(qr, sr, qwT, sw, o, dx)
+        xT, xs = fq.grouped_transpose_quant_fp8_alloc(qa, sa, o)
+        dw = torch.empty((o.numel() - 1, N, K), dtype=torch.bfloat16, device=DEV)
+        fq.grouped_linear_wgrad(qc, sc, xT, xs, o, dw)
+        torch.cuda.synchronize()
+        assert fq.device_error() == fq.FP8Q_OK
+        return y, dx, dw
+
+    y, dx, dw = run(qw, sw, qwT, o)
+    y1, dx1, dw1 = run(qw1, sw1, qwT1, o_used)
+    assert same_bits(y, y1) and same_bits(dx, dx1) and same_bits(dw[used].contiguous(), dw1)
+    rest = np.setdiff1d(np.arange(E), used)
+    assert torch.all(dw[rest] == 0)
+    with pytest.raises(ValueError):  # one more does not fit the table
+        fq.grouped_transpose_quant_bf16_alloc(dy, torch.zeros(E + 2, dtype=torch.int32, device=DEV))
+
+
+def test_calls_in_a_row_see_each_other(fq):
+    """Kernels whose launches overlap the end of the one before: a stream updated in place
+    forty times without a wait, a consumer after every step, inputs overwritten behind it."""
+    M, H, N, E = 300, 1024, 256, 3
+    x = workloads.activations_bf16((M, H), 0, 3180, DEV)
+    gamma = workloads.gamma_bf16(H, 0, 3181, DEV)
+    qw, sw, _ = weights(fq, E, N, H, 3182)
+    o = dev_offsets(np.array([0, 100, 101, 300], np.int32))
+    res = torch.zeros_like(x)
+    q = torch.empty((M, H), dtype=torch.uint8, device=DEV)
+    s = torch.empty((H // 128, M), device=DEV)
+    ys = [torch.zeros((M, N), dtype=torch.bfloat16, device=DEV) for _ in range(40)]
+    for y in ys:
+        fq.add_rmsnorm_quant(x, res, gamma, 1e-5, res, q, s)
+        fq.grouped_linear_fwd(q, s, qw, sw, o, y)
+        q.fill_(0x7F)
+    want = torch.zeros_like(x)
+    for y in ys:
+        want = (want.float() + x.float()).to(torch.bfloat16)
+        q1, s1 = fq.rmsnorm_quant_alloc(want, gamma, 1e-5)
+        torch.cuda.synchronize()
+        y1 = torch.zeros_like(y)
+        fq.grouped_linear_fwd(q1, s1, qw, sw, o, y1)
+        torch.cuda.synchronize()
+        assert same_bits(y, y1)
+    assert same_bits(res, want)
+
+
 def test_no_rows_at_all(fq):
     M, N, K, E = 0, 256, 128, 3
     o = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
