@@ -3162,10 +3162,11 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
 //          between warps; lane 8g + c holds columns 4c .. 4c + 3 of two rows of every eight,
 //          rows 0, 4, 2, 6 and the next one for g = 0 .. 3 (which with the swizzle puts the
 //          two g of a half-warp's 8-byte reads into different halves of the row).
-// 60.7 us (4.5 TB/s) at 16384 x 4096 over 8 experts, 10.6 us at 301 x 3584 over 16; the
-// dense kernel's layout (eight column warps that meet twice a tile) took 60.7 and 11.7. The
-// tile copies alone take 29.7, with the rows 40.5, with the columns 45.0: both passes are
-// bound by their instructions (about 15 per element in all), not by the memory.
+// 56.2 us (4.9 TB/s) at 16384 x 4096 over 8 experts, 10.3 us at 301 x 3584 over 16; with
+// quot2's three operations 60.7 and 10.6, in the dense kernel's layout (eight column warps
+// that meet twice a tile) 60.7 and 11.7. Of the 60.7 the tile copies alone took 29.7, with
+// the rows 40.5, with the columns 45.0: both passes are bound by their instructions (about
+// 15 per element in all, now 14), not by the memory.
 constexpr int kGgStages = 4;
 constexpr int kGgThreads = 640;
 constexpr uint32_t kGgRegsRow = 88, kGgRegsCol = 136, kGgRegsRest = 24;
@@ -3176,39 +3177,148 @@ constexpr uint32_t kGgTile = 2 * kGgBox;
 constexpr uint32_t kGgOffCol = kGgStages * kGgTile;         // 8 x [32 columns][128 codes]
 constexpr uint32_t kGgOffRow = kGgOffCol + 8 * 32 * 128;    // 8 x [16 rows][128 codes]
 constexpr uint32_t kGgOffTab = kGgOffRow + 8 * 16 * 128;    // scale and reciprocal tables
-constexpr uint32_t kGgOffRows = kGgOffTab + 256 * 4;        // int2 per stage
+constexpr uint32_t kGgOffRows = kGgOffTab + 384 * 4;        // int2 per stage
 constexpr uint32_t kGgOffBar = kGgOffRows + kGgStages * 8;
 constexpr uint32_t kGgOffOffsets = kGgOffBar + 2 * kGgStages * 8 + 16;
 constexpr size_t grouped_grad_smem(int E) { return 1024 + kGgOffOffsets + group_table_bytes(E); }
 static_assert(grouped_grad_smem(kMaxExperts) <= 232448, "shared memory budget of one sm_100 CTA");
 
-// Four codes of a row: two packed BF16 pairs with the scales of their columns.
-template <bool kDiv>
-__device__ __forceinline__ uint32_t codes4_cols(uint2 w, const GroupScale (&g)[4]) {
-  const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-  float t[4];
-  if (kDiv) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) t[c] = g[c].small ? __fdiv_rn(x[c], g[c].s) : quot(x[c], g[c]);
-  } else {
-    quot2(x[0], x[1], g[0], g[1], t[0], t[1]);
-    quot2(x[2], x[3], g[2], g[3], t[2], t[3]);
+// 1/s as a sum of two floats, for s = fl32(amax/448) of amax = 1 + i/128: hi the reciprocal
+// rounded toward zero, lo = fl32(1/s - hi) >= 0. fma(x, hi, fl32(x lo)) then has the E4M3
+// code of the IEEE quotient x/s for every BF16 |x| <= amax and keeps the sign of a zero (the
+// test suite derives both tables and checks every pair): two operations instead of quot's
+// three. (A single product with the best float per i gives the codes for 121 of the 128.)
+__constant__ float kRecipHi[128] = {
+    0x1.bffffep+8f, 0x1.bc86fp+8f, 0x1.b91b92p+8f, 0x1.b5bd8ep+8f, 0x1.b26c9ap+8f,
+    0x1.af286ap+8f, 0x1.abf0b8p+8f, 0x1.a8c534p+8f, 0x1.a5a5a4p+8f, 0x1.a291cp+8f,
+    0x1.9f8946p+8f, 0x1.9c8bf6p+8f, 0x1.999998p+8f, 0x1.96b1eep+8f, 0x1.93d4bap+8f,
+    0x1.9101c8p+8f, 0x1.8e38e2p+8f, 0x1.8b79d2p+8f, 0x1.88c46p+8f, 0x1.86186p+8f,
+    0x1.83759ep+8f, 0x1.80dbeap+8f, 0x1.7e4b16p+8f, 0x1.7bc2f6p+8f, 0x1.79435ep+8f,
+    0x1.76cc2p+8f, 0x1.745d16p+8f, 0x1.71f616p+8f, 0x1.6f96f8p+8f, 0x1.6d3f96p+8f,
+    0x1.6aefccp+8f, 0x1.68a772p+8f, 0x1.666664p+8f, 0x1.642c84p+8f, 0x1.61f9aep+8f,
+    0x1.5fcdbcp+8f, 0x1.5da894p+8f, 0x1.5b8a14p+8f, 0x1.59721ep+8f, 0x1.576092p+8f,
+    0x1.555554p+8f, 0x1.535048p+8f, 0x1.51515p+8f, 0x1.4f5852p+8f, 0x1.4d6534p+8f,
+    0x1.4b77dcp+8f, 0x1.49902ep+8f, 0x1.47ae14p+8f, 0x1.45d174p+8f, 0x1.43fa36p+8f,
+    0x1.422844p+8f, 0x1.405b88p+8f, 0x1.3e93e8p+8f, 0x1.3cd152p+8f, 0x1.3b13bp+8f,
+    0x1.395aeep+8f, 0x1.37a6f4p+8f, 0x1.35f7b2p+8f, 0x1.344d12p+8f, 0x1.32a704p+8f,
+    0x1.31057p+8f, 0x1.2f684ap+8f, 0x1.2dcf7ep+8f, 0x1.2c3af8p+8f, 0x1.2aaaaap+8f,
+    0x1.291e82p+8f, 0x1.27966ep+8f, 0x1.26126p+8f, 0x1.249248p+8f, 0x1.231616p+8f,
+    0x1.219dbcp+8f, 0x1.20292ap+8f, 0x1.1eb852p+8f, 0x1.1d4b24p+8f, 0x1.1be194p+8f,
+    0x1.1a7b96p+8f, 0x1.191918p+8f, 0x1.17ba1p+8f, 0x1.165e72p+8f, 0x1.15062ep+8f,
+    0x1.13b13ap+8f, 0x1.125f8ap+8f, 0x1.11111p+8f, 0x1.0fc5c2p+8f, 0x1.0e7d94p+8f,
+    0x1.0d387cp+8f, 0x1.0bf66ep+8f, 0x1.0ab75ep+8f, 0x1.097b42p+8f, 0x1.08421p+8f,
+    0x1.070bbep+8f, 0x1.05d84p+8f, 0x1.04a79p+8f, 0x1.0379ap+8f, 0x1.024e6ap+8f, 0x1.0125ep+8f,
+    0x1p+8f, 0x1.fdb974p+7f, 0x1.fb7812p+7f, 0x1.f93bc6p+7f, 0x1.f7047cp+7f, 0x1.f4d228p+7f,
+    0x1.f2a4bap+7f, 0x1.f07c1ep+7f, 0x1.ee5846p+7f, 0x1.ec3922p+7f, 0x1.ea1ea2p+7f,
+    0x1.e808b4p+7f, 0x1.e5f75p+7f, 0x1.e3ea64p+7f, 0x1.e1e1ep+7f, 0x1.dfddb8p+7f,
+    0x1.dddddep+7f, 0x1.dbe242p+7f, 0x1.d9ead6p+7f, 0x1.d7f79p+7f, 0x1.d60864p+7f,
+    0x1.d41d4p+7f, 0x1.d2361cp+7f, 0x1.d052eap+7f, 0x1.ce739ep+7f, 0x1.cc9826p+7f,
+    0x1.cac082p+7f, 0x1.c8ec9ep+7f, 0x1.c71c7p+7f, 0x1.c54ffp+7f, 0x1.c3870ep+7f,
+    0x1.c1c1c2p+7f,
+};
+__constant__ float kRecipLo[128] = {
+    0x1.600002p-17f, 0x1.ad833ep-16f, 0x1.2d812p-19f, 0x1.e8d916p-16f, 0x1.50a1bep-18f,
+    0x1.ca1af2p-16f, 0x1.9c6dbcp-19f, 0x1.d00b78p-16f, 0x1.426f9cp-16f, 0x1.b2b7f2p-17f,
+    0x1.9f36bp-16f, 0x1.e41f52p-16f, 0x1.99999ap-16f, 0x1.214fd4p-17f, 0x1.b4bd22p-18f,
+    0x1.f173f6p-16f, 0x1.e6b75p-16f, 0x1.1e8cbp-16f, 0x1.84ec8cp-16f, 0x1.861862p-16f,
+    0x1.ca2506p-16f, 0x1.a7e14ap-18f, 0x1.93232ep-16f, 0x1.d669bep-16f, 0x1.3f1d14p-16f,
+    0x1.b409eep-17f, 0x1.45d174p-16f, 0x1.b8238cp-16f, 0x1.1ac2e8p-17f, 0x1.5a3e0cp-16f,
+    0x1.c191a8p-18f, 0x1.2a41aep-16f, 0x1.d70a3ep-16f, 0x1.90b216p-16f, 0x1.7e6178p-18f,
+    0x1.3a39ep-16f, 0x1.964f7ep-16f, 0x1.fc082ap-16f, 0x1.9fadf4p-16f, 0x1.4b9752p-17f,
+    0x1.555556p-16f, 0x1.3645cap-16f, 0x1.25aa3p-17f, 0x1.9753c6p-16f, 0x1.d2dd4p-16f,
+    0x1.343c98p-16f, 0x1.36c212p-17f, 0x1.eb851ep-18f, 0x1.a723f8p-17f, 0x1.18a2fap-18f,
+    0x1.9d6d34p-17f, 0x1.6f2546p-20f, 0x1.e87c66p-16f, 0x1.028a24p-16f, 0x1.3b13b2p-16f,
+    0x1.f034f6p-19f, 0x1.e00f8p-19f, 0x1.31d6b2p-18f, 0x1.79dbb6p-16f, 0x1.719c6cp-17f,
+    0x1.fa349ep-16f, 0x1.da12f6p-16f, 0x1.0cbc76p-16f, 0x1.6afe5ap-17f, 0x1.e38e3ap-18f,
+    0x1.74e22ap-19f, 0x1.6aaebcp-16f, 0x1.8b1ca2p-17f, 0x1.24924ap-16f, 0x1.c2a084p-16f,
+    0x1.c0d7a8p-19f, 0x1.15c414p-18f, 0x1.9652bep-20f, 0x1.77b3dp-16f, 0x1.3176ap-16f,
+    0x1.1a7b96p-20f, 0x1.714922p-16f, 0x1.f1453ep-17f, 0x1.4a1acap-19f, 0x1.29969ap-16f,
+    0x1.92ef56p-16f, 0x1.552354p-20f, 0x1.111112p-16f, 0x1.a89358p-16f, 0x1.41e41ep-16f,
+    0x1.acb422p-17f, 0x1.b365p-19f, 0x1.0f85fcp-17f, 0x1.02754cp-20f, 0x1.08421p-17f,
+    0x1.1493dp-17f, 0x1.03485ep-16f, 0x1.247986p-19f, 0x1.290bd2p-16f, 0x1.0d86b4p-17f,
+    0x1.dd3b28p-16f, 0.0f, 0x1.c1e9a8p-17f, 0x1.3f2206p-17f, 0x1.06ae9ep-17f, 0x1.98773ap-21f,
+    0x1.6308dap-17f, 0x1.cc1574p-19f, 0x1.07c1fp-17f, 0x1.27447ep-17f, 0x1.1dc9bp-17f,
+    0x1.7c44e6p-17f, 0x1.7488aep-17f, 0x1.693d1ep-17f, 0x1.0680fap-17f, 0x1.e1e1e2p-17f,
+    0x1.ceb132p-17f, 0x1.b97532p-18f, 0x1.5702dep-17f, 0x1.54e3f4p-19f, 0x1.771008p-17f,
+    0x1.eaf296p-20f, 0x1.d41d42p-17f, 0x1.9cac42p-17f, 0x1.2cbc12p-17f, 0x1.3502f2p-19f,
+    0x1.bcb6e2p-17f, 0x1.3c686ap-20f, 0x1.4e1p-18f, 0x1.c71c72p-17f, 0x1.08692cp-19f,
+    0x1.ff861cp-18f, 0x1.1465b8p-17f,
+};
+constexpr int kRecipMinExp = -71, kRecipMaxExp = 60;  // amax exponents that take this path
+
+struct GroupRecip {
+  float s, hi, lo;  // scale, and its reciprocal as hi + lo
+  bool small;       // amax outside the exponents above: quotients by IEEE division
+};
+
+// Tables in shared memory: tab[0..127] the scale mantissas, [128..255] hi, [256..383] lo.
+__device__ __forceinline__ GroupRecip group_recip_sm(float amax, const float* tab) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = static_cast<int>(b >> 23) - 127;
+  const uint32_t i = (b >> 16) & 0x7Fu;
+  const bool out = (e < kRecipMinExp || e > kRecipMaxExp) && b != 0;
+  const float p = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
+  GroupRecip g;
+  g.s = __uint_as_float(__float_as_uint(tab[i]) + static_cast<uint32_t>((e - 6) << 23));
+  g.hi = __fmul_rn(tab[128 + i], p);
+  g.lo = __fmul_rn(tab[256 + i], p);
+  g.small = false;
+  if (b == 0) {  // an all-zero group: s = 1, and 0 / 1 is exact either way
+    g.s = g.hi = 1.0f;
+    g.lo = 0.0f;
   }
-  return cvt_e4m3x4(t[0], t[1], t[2], t[3]);
+  if (__any_sync(kFull, out)) {
+    if (out) {
+      g.s = group_scale(amax).s;
+      g.hi = g.lo = 0.0f;
+      g.small = true;
+    }
+  }
+  return g;
 }
 
-// A column warp's tile where some column has a tiny scale (divides): rolled up and out of
-// line, away from the registers of the usual path.
+// x0/s0 and x1/s1 for BF16 values.
+__device__ __forceinline__ void quot2_recip(float x0, float x1, const GroupRecip& g0,
+                                            const GroupRecip& g1, float& t0, float& t1) {
+  mul2(t0, t1, x0, x1, g0.lo, g1.lo);
+  fma2(t0, t1, x0, x1, g0.hi, g1.hi);
+}
+
+// Codes of 8 BF16 values of one group; kSmall: some lane of the warp has to divide.
+template <bool kSmall>
+__device__ __forceinline__ uint2 codes8_recip(const uint4& w, const GroupRecip& g) {
+  float v[8], t[8];
+  unpack_bf16x8(w, v);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) quot2_recip(v[i], v[i + 1], g, g, t[i], t[i + 1]);
+  if (kSmall) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = g.small ? __fdiv_rn(v[i], g.s) : t[i];
+  }
+  return make_uint2(cvt_e4m3x4(t[0], t[1], t[2], t[3]), cvt_e4m3x4(t[4], t[5], t[6], t[7]));
+}
+
+// Four codes of a row: two packed BF16 pairs with the scales of their columns.
+__device__ __forceinline__ uint32_t codes4_cols(uint2 w, const GroupRecip (&g)[4]) {
+  float t[4];
+  quot2_recip(bf16_lo(w.x), bf16_hi(w.x), g[0], g[1], t[0], t[1]);
+  quot2_recip(bf16_lo(w.y), bf16_hi(w.y), g[2], g[3], t[2], t[3]);
+  return cvt_e4m3x4(t[0], t[1], t[2], t[3]);
+}
+__device__ __forceinline__ uint32_t codes4_cols_div(uint2 w, const float (&s)[4]) {
+  return cvt_e4m3x4(__fdiv_rn(bf16_lo(w.x), s[0]), __fdiv_rn(bf16_hi(w.x), s[1]),
+                    __fdiv_rn(bf16_lo(w.y), s[2]), __fdiv_rn(bf16_hi(w.y), s[3]));
+}
+
+// A column warp's tile where some column has to divide: rolled up and out of line, away
+// from the registers of the usual path.
 __device__ __noinline__ void grad_tile_div(const uint8_t* worda, const uint8_t* wordb,
                                            const float* amax, int rows, int gr, int row0,
                                            uint8_t* orow, int col) {
   const RowsToColumns<true> to_columns(gr);
-  GroupScale g[4];
+  float sc[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    g[c] = group_scale(amax[c]);
-    g[c].small = true;
-  }
+  for (int c = 0; c < 4; ++c) sc[c] = group_scale(amax[c]).s;
 #pragma unroll 1
   for (int j = 0; j < 16; ++j) {
     uint2 wa = *reinterpret_cast<const uint2*>(worda + j * 1024);
@@ -3216,7 +3326,7 @@ __device__ __noinline__ void grad_tile_div(const uint8_t* worda, const uint8_t* 
     if (8 * j + row0 >= rows) wa = make_uint2(0u, 0u);
     if (8 * j + row0 + 1 >= rows) wb = make_uint2(0u, 0u);
     uint32_t o0, o1;
-    to_columns(codes4_cols<true>(wa, g), codes4_cols<true>(wb, g), o0, o1);
+    to_columns(codes4_cols_div(wa, sc), codes4_cols_div(wb, sc), o0, o1);
     *reinterpret_cast<uint2*>(orow + (((j >> 1) ^ (col & 7)) << 4) + 8 * (j & 1)) = make_uint2(o0, o1);
   }
 }
@@ -3241,7 +3351,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x >= 128 && threadIdx.x < 256) {
     tab[threadIdx.x - 128] = kScaleMant[threadIdx.x - 128];
-    tab[threadIdx.x] = kRecipMant[threadIdx.x - 128];
+    tab[threadIdx.x] = kRecipHi[threadIdx.x - 128];
+    tab[threadIdx.x + 128] = kRecipLo[threadIdx.x - 128];
   }
   if (threadIdx.x == kGgThreads - 1) {  // the copies' descriptors, while the offsets come
     prefetch_tensormap(&tmD);
@@ -3318,7 +3429,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
         const float amax = half_row_amax(w);
         __syncwarp();  // every lane's reads of the tile are complete (their values are used)
         if (lane == 0) mbar_arrive(empty + b);
-        const GroupScale g = group_scale_bf16_sm(amax, tab);
+        const GroupRecip g = group_recip_sm(amax, tab);
         const bool small = __any_sync(kFull, g.small);
         const int64_t mb = t / NB, nb = t - mb * NB;
         const int m0 = rows.x + rw * 16;
@@ -3331,8 +3442,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
         uint8_t* dst = grp.q_row + static_cast<int64_t>(m0 + rl) * N + c0;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const uint2 c = small ? codes8_words<true>(w[j], g) : codes8_words<false>(w[j], g);
-          const uint2 d = small ? codes8_words<true>(w[j + 1], g) : codes8_words<false>(w[j + 1], g);
+          const uint2 c = small ? codes8_recip<true>(w[j], g) : codes8_recip<false>(w[j], g);
+          const uint2 d = small ? codes8_recip<true>(w[j + 1], g) : codes8_recip<false>(w[j + 1], g);
           const uint4 v = make_uint4(c.x, c.y, d.x, d.y);
           if (whole)
             *reinterpret_cast<uint4*>(out + rl * 128 + (((4 * hh + (j >> 1)) ^ (rl & 7)) << 4)) = v;
@@ -3399,9 +3510,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
       }
       const float amax[4] = {fabsf(bf16_lo(m0)), fabsf(bf16_hi(m0)), fabsf(bf16_lo(m1)),
                              fabsf(bf16_hi(m1))};
-      GroupScale g[4];
+      GroupRecip g[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) g[c] = group_scale_bf16_sm(amax[c], tab);
+      for (int c = 0; c < 4; ++c) g[c] = group_recip_sm(amax[c], tab);
       const int64_t mb = t / NB, nb = t - mb * NB;
       const int64_t c0 = nb * 128 + 32 * cw;
       if (gr == 0 && c0 + 4 * c8 < N)  // N is a multiple of 16: the four are in or out
@@ -3423,7 +3534,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
               const int j = 2 * j2 + jj;
-              to_columns(codes4_cols<false>(w[2 * j], g), codes4_cols<false>(w[2 * j + 1], g),
+              to_columns(codes4_cols(w[2 * j], g), codes4_cols(w[2 * j + 1], g),
                          o[2 * jj], o[2 * jj + 1]);
             }
           }

@@ -324,6 +324,25 @@ def test_tiny_scales(fq, oracle_mod):
         g += n
 
 
+def test_huge_scales(fq, oracle_mod):
+    """Values over 2^60 take the division path, beside ordinary ones and zeros."""
+    off, M, E = route("spare")
+    N = 272
+    x = workloads.activations_bf16((M, N), 0, 3066, DEV)
+    x[:, 3:200:5] *= 1e22
+    x[10:30] *= 1e10
+    x[40, :] = 0
+    x[41, ::2] = -0.0
+    o = dev_offsets(off)
+    P = fq.grouped_padded_rows(M, E)
+    q = torch.full((M, N), 77, dtype=torch.uint8, device=DEV)
+    s = torch.full((-(-N // 128), fq.lds_for(M)), -1.0, device=DEV)
+    qT = torch.full((N, P), 77, dtype=torch.uint8, device=DEV)
+    sT = torch.full((P // 128, N), -1.0, device=DEV)
+    fq.grouped_transpose_quant_bf16(x, o, q, s, qT, sT)
+    check_rows_and_columns(oracle_mod, x, off, q, s, qT, sT)
+
+
 def test_values_of_other_experts_do_not_leak(fq, oracle_mod):
     """NaN in the neighbours' rows (and in nobody's) changes nothing in an expert's groups."""
     off, M, E = route("spare")
