@@ -557,41 +557,46 @@ def linear_wgrad_acc_f32(qdyT, sdy_c, qxT, sx_c, dw, stream=None):
 def _row_stride(t, rows, cols, name):
     """Row stride of a [rows, cols] matrix with dense rows (a single row has none: its
     length)."""
+    if t.is_contiguous():
+        return cols
     r, c = t.stride()
     if c != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
     return r if rows > 1 else cols
 
 
-def _run(fn, where, stream, ref, *args):
-    """Call `fn` on the device of `ref` (the current one or not), on `stream` or that
-    device's current stream."""
-    dev = ref.get_device()
-    if dev == torch.cuda.current_device():
-        _check(fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream), where)
-    else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream), where)
-
-
 def _raw_stream(dev):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-# The same without building a Stream object (3 us of a small call), where torch has it.
+# The same without a Stream object, and the device without the check that CUDA is up (it is:
+# the operands lie there): 3 us of a small call, where torch has them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _pointers(*named):
-    """Device pointers of the operands (0 for None), which all lie on the first one's
-    device."""
-    dev = named[0][0].get_device()
+def _run(fn, where, stream, dev, *args):
+    """Call `fn` on device `dev` (the current one or not), on `stream` or that device's
+    current stream."""
+    if dev == _current_device():
+        status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status != FP8Q_OK:
+        raise Fp8qError(status, where)
+
+
+def _device(names, *operands):
+    """The CUDA device on which all operands (None: not given) lie."""
+    dev = operands[0].get_device()
     if dev < 0:
         raise ValueError("libfp8q takes CUDA tensors (device pointers)")
-    for t, n in named:
+    for t in operands:
         if t is not None and t.get_device() != dev:
-            raise ValueError("%s must be on cuda:%d, got %s" % (n, dev, t.device))
-    return [None if t is None else t.data_ptr() for t, _ in named]
+            name = [n for n, o in zip(names.split(), operands) if o is t][0]
+            raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    return dev
 
 
 _T, _BF16, _U8, _F32 = torch.Tensor, torch.bfloat16, torch.uint8, torch.float32
@@ -659,11 +664,11 @@ def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
         _exact_dense(gamma, (H,), _BF16, "gamma")
         _exact_dense(q, shape, _U8, "q")
     lds = _scales_dense(s, _groups(H), M, "s")
-    px, pr, pg, ph, pq, ps = _pointers((x, "x"), (res, "res"), (gamma, "gamma"), (h, "h"),
-                                       (q, "q"), (s, "s"))
-    _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, x, px, pr, pg, M, H,
-         _row_stride(x, M, H, "x"), _row_stride(res, M, H, "res"), eps, ph,
-         _row_stride(h, M, H, "h"), pq, ps, lds)
+    dev = _device("x res gamma h q s", x, res, gamma, h, q, s)
+    _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, dev, x.data_ptr(),
+         res.data_ptr(), gamma.data_ptr(), M, H, _row_stride(x, M, H, "x"),
+         _row_stride(res, M, H, "res"), float(eps), h.data_ptr(), _row_stride(h, M, H, "h"),
+         q.data_ptr(), s.data_ptr(), lds)
 
 
 def add_rmsnorm_quant_alloc(x, res, gamma, eps, stream=None):
@@ -720,10 +725,10 @@ def grouped_linear_fwd(qa, sa, qw, sw, offsets, y, stream=None):
     E, N, K = _grouped_weight(qw, sw, offsets, "qw", 1)
     M, lds = _grouped_rows(qa, sa, K, "qa", "sa")
     _exact(y, (M, N), torch.bfloat16, "y")
-    pa, psa, pw, psw, po, py = _pointers((qa, "qa"), (sa, "sa"), (qw, "qw"), (sw, "sw"),
-                                         (offsets, "offsets"), (y, "y"))
-    _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, qa, pa, psa,
-         lds, pw, psw, po, E, M, N, K, py, _row_stride(y, M, N, "y"))
+    dev = _device("qa sa qw sw offsets y", qa, sa, qw, sw, offsets, y)
+    _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, dev, qa.data_ptr(),
+         sa.data_ptr(), lds, qw.data_ptr(), sw.data_ptr(), offsets.data_ptr(), E, M, N, K,
+         y.data_ptr(), _row_stride(y, M, N, "y"))
 
 
 def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
@@ -732,10 +737,10 @@ def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
     E, N, K = _grouped_weight(qwT, sw, offsets, "qwT", 2)
     M, lds = _grouped_rows(qdy, sdy, N, "qdy", "sdy")
     _exact(dx, (M, K), torch.bfloat16, "dx")
-    pa, psa, pw, psw, po, px = _pointers((qdy, "qdy"), (sdy, "sdy"), (qwT, "qwT"), (sw, "sw"),
-                                         (offsets, "offsets"), (dx, "dx"))
-    _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, qdy, pa, psa,
-         lds, pw, psw, po, E, M, N, K, px, _row_stride(dx, M, K, "dx"))
+    dev = _device("qdy sdy qwT sw offsets dx", qdy, sdy, qwT, sw, offsets, dx)
+    _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, dev, qdy.data_ptr(),
+         sdy.data_ptr(), lds, qwT.data_ptr(), sw.data_ptr(), offsets.data_ptr(), E, M, N, K,
+         dx.data_ptr(), _row_stride(dx, M, K, "dx"))
 
 
 def _grouped_columns(qT, sT, rows, name_q, name_s):
@@ -765,10 +770,11 @@ def grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, strea
         _exact_dense(q_row, shape, _U8, "q_row")
         lds_row = _scales_dense(s_row, _groups(N), M, "s_row")
     P = _grouped_columns(q_colT, s_col, N, "q_colT", "s_col")
-    pd, po, pq, ps, pqT, psT = _pointers((dy, "dy"), (offsets, "offsets"), (q_row, "q_row"),
-                                         (s_row, "s_row"), (q_colT, "q_colT"), (s_col, "s_col"))
-    _run(_lib.fp8q_grouped_transpose_quant_bf16, "fp8q_grouped_transpose_quant_bf16", stream, dy,
-         pd, po, E, M, N, _row_stride(dy, M, N, "dy"), pq, ps, lds_row, pqT, psT, P)
+    dev = _device("dy offsets q_colT s_col q_row s_row", dy, offsets, q_colT, s_col, q_row, s_row)
+    _run(_lib.fp8q_grouped_transpose_quant_bf16, "fp8q_grouped_transpose_quant_bf16", stream, dev,
+         dy.data_ptr(), offsets.data_ptr(), E, M, N, _row_stride(dy, M, N, "dy"),
+         None if q_row is None else q_row.data_ptr(), None if s_row is None else s_row.data_ptr(),
+         lds_row, q_colT.data_ptr(), s_col.data_ptr(), P)
 
 
 def grouped_transpose_quant_bf16_alloc(dy, offsets, want_row=True, stream=None):
@@ -792,10 +798,10 @@ def grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream=None):
     K = q.shape[1]
     M, lds = _grouped_rows(q, s, K, "q", "s")
     P = _grouped_columns(qT, sT, K, "qT", "sT")
-    pq, ps, po, pqT, psT = _pointers((q, "q"), (s, "s"), (offsets, "offsets"), (qT, "qT"),
-                                     (sT, "sT"))
-    _run(_lib.fp8q_grouped_transpose_quant_fp8, "fp8q_grouped_transpose_quant_fp8", stream, q,
-         pq, ps, po, E, M, K, lds, pqT, psT, P)
+    dev = _device("q s offsets qT sT", q, s, offsets, qT, sT)
+    _run(_lib.fp8q_grouped_transpose_quant_fp8, "fp8q_grouped_transpose_quant_fp8", stream, dev,
+         q.data_ptr(), s.data_ptr(), offsets.data_ptr(), E, M, K, lds, qT.data_ptr(),
+         sT.data_ptr(), P)
 
 
 def grouped_transpose_quant_fp8_alloc(q, s, offsets, stream=None):
@@ -824,10 +830,10 @@ def grouped_linear_wgrad(qdyT, sdy_c, qxT, sx_c, offsets, dw, stream=None):
     if dw.shape[0] != E:
         raise ValueError("dw holds %d experts, offsets %d" % (dw.shape[0], E))
     _exact_dense(dw, (E, N, K), torch.bfloat16, "dw")
-    pa, psa, pb, psb, po, pw = _pointers((qdyT, "qdyT"), (sdy_c, "sdy_c"), (qxT, "qxT"),
-                                         (sx_c, "sx_c"), (offsets, "offsets"), (dw, "dw"))
-    _run(_lib.fp8q_grouped_linear_wgrad, "fp8q_grouped_linear_wgrad", stream, qdyT, pa, psa, pb,
-         psb, po, E, P, N, K, pw, K)
+    dev = _device("qdyT sdy_c qxT sx_c offsets dw", qdyT, sdy_c, qxT, sx_c, offsets, dw)
+    _run(_lib.fp8q_grouped_linear_wgrad, "fp8q_grouped_linear_wgrad", stream, dev,
+         qdyT.data_ptr(), sdy_c.data_ptr(), qxT.data_ptr(), sx_c.data_ptr(), offsets.data_ptr(),
+         E, P, N, K, dw.data_ptr(), K)
 
 
 def debug_wait_timeout(limit_ns: int, stream=None) -> int:
