@@ -670,6 +670,82 @@ def test_offsets_out_of_order_are_clamped_and_reported(fq, bad):
     assert fq.device_error() == fq.FP8Q_OK
 
 
+def test_wgrad_drops_groups_past_its_columns(fq):
+    """Operands with fewer columns than the offsets need: the groups past the end are left
+    out and reported, the others are as they would be."""
+    N, K, E = 128, 256, 3
+    off = np.array([0, 130, 300, 420], np.int32)          # 2, 2 and 1 groups
+    o = dev_offsets(off)
+    M = int(off[-1])
+    dy = workloads.gradients_bf16((M, N), 1e-3, 0, 3185, DEV)
+    x = workloads.activations_bf16((M, K), 0, 3186, DEV)
+    _, _, c, cs = fq.grouped_transpose_quant_bf16_alloc(dy, o, want_row=False)
+    t, ts = fq.grouped_transpose_quant_fp8_alloc(*fq.quant_act_1x128_alloc(x), o)
+    dw = torch.empty((E, N, K), dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_wgrad(c, cs, t, ts, o, dw)
+    assert fq.device_error() == fq.FP8Q_OK
+    short = torch.full_like(dw, 7.5)
+    P = 3 * 128                                           # expert 1 keeps one of two, 2 none
+    fq.grouped_linear_wgrad(c[:, :P].contiguous(), cs[:3].contiguous(), t[:, :P].contiguous(),
+                            ts[:3].contiguous(), o, short)
+    assert fq.device_error() == fq.FP8Q_ERR_OFFSETS
+    assert same_bits(short[0], dw[0]) and torch.all(short[2] == 0)
+    one = fq.linear_wgrad_alloc(c[:, 256:P].contiguous(), cs[2:3].contiguous(),
+                                t[:, 256:P].contiguous(), ts[2:3].contiguous())
+    assert same_bits(short[1], one)
+
+
+def test_elements_past_32_bits(fq):
+    """Arrays of more than 2^31 elements: the last rows and columns against small calls."""
+    M, wide, N, K = 70000, 32768, 128, 256
+    counts = [M - 300, 300]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    o, lo = dev_offsets(off), int(off[1])
+    o_last = dev_offsets(np.array([0, 0, 300], np.int32))
+    qw, sw, qwT = weights(fq, 2, N, K, 3190)
+    x = workloads.activations_bf16((M, K), 0, 3191, DEV)
+    qa, sa = fq.quant_act_1x128_alloc(x)
+    big = torch.zeros((M, wide), dtype=torch.bfloat16, device=DEV)   # 2.29e9 elements
+    fq.grouped_linear_fwd(qa, sa, qw, sw, o, big[:, wide - N:])
+    q1, s1 = fq.quant_act_1x128_alloc(x[lo:].contiguous())
+    y1 = torch.zeros((300, N), dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_fwd(q1, s1, qw, sw, o_last, y1)
+    assert same_bits(big[lo:, wide - N:].contiguous(), y1)
+    # the same rows through the strip kernel (few rows per expert of a large buffer)
+    o_many = dev_offsets(np.concatenate([[lo] * 1000, [M] * 25]).astype(np.int32))
+    many_w = qw[1:].expand(1024, N, K).contiguous()
+    many_s = sw[1:].expand(1024, 1, K // 128).contiguous()
+    big.zero_()
+    fq.grouped_linear_fwd(qa, sa, many_w, many_s, o_many, big[:, wide - N:])
+    assert same_bits(big[lo:, wide - N:].contiguous(), y1)
+    assert fq.device_error() == fq.FP8Q_OK
+    # quantizers: 2.29e9 codes each way
+    for i in range(0, M, 7000):
+        big[i:i + 7000].normal_()
+    q, s, qT, sT = fq.grouped_transpose_quant_bf16_alloc(big, o)
+    r = fq.grouped_transpose_quant_bf16_alloc(big[lo:].contiguous(), o_last)
+    g0 = -(-lo // 128)
+    assert torch.equal(q[lo:], r[0]) and torch.equal(s[:, lo:M], r[1][:, :300])
+    assert torch.equal(qT[-3:, 128 * g0:128 * g0 + 384], r[2][-3:, :384])
+    assert torch.equal(sT[g0:g0 + 3], r[3][:3])
+    t, ts = fq.grouped_transpose_quant_fp8_alloc(q, s, o)
+    s_last = torch.empty((wide // 128, 300), device=DEV)
+    s_last.copy_(s[:, lo:M])
+    t1, ts1 = fq.grouped_transpose_quant_fp8_alloc(q[lo:].contiguous(), s_last, o_last)
+    assert torch.equal(t[-3:, 128 * g0:128 * g0 + 384], t1[-3:, :384])
+    assert torch.equal(ts[g0:g0 + 3], ts1[:3])
+    # the norm: rows of more than 2^31 elements in all, in place
+    gamma = workloads.gamma_bf16(16384, 0, 3192, DEV)
+    view = big[:, :16384]
+    last = big[-5:, :16384].clone()
+    qn = torch.empty((M, 16384), dtype=torch.uint8, device=DEV)
+    sn = torch.empty((128, M), device=DEV)
+    fq.add_rmsnorm_quant(view, view, gamma, 1e-5, view, qn, sn)
+    h, q5, s5 = fq.add_rmsnorm_quant_alloc(last, last, gamma, 1e-5)
+    assert same_bits(big[-5:, :16384].contiguous(), h) and torch.equal(qn[-5:], q5)
+    assert torch.equal(sn[:, -5:], s5[:, :5]) and fq.device_error() == fq.FP8Q_OK
+
+
 def test_most_experts(fq):
     """1024 experts (the table's limit), most of them without rows, against the same rows in
     a call with only the experts that have some."""
