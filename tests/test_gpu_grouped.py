@@ -362,7 +362,7 @@ def test_values_of_other_experts_do_not_leak(fq, oracle_mod):
     # and in the products: NaN codes in the rows around
     K = 384
     qw, sw, _ = weights(fq, E, N, K, 3071)
-    qa, sa = fq.quant_act_1x128_alloc(workloads.activations_bf16((M, K), 0, 3072, DEV))
+    qa, sa = fq.quant_act_1x128_alloc(workloads.activations_bf16((M, K), 0, 3172, DEV))
     y = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
     fq.grouped_linear_fwd(qa, sa, qw, sw, o, y)
     qb, sb = torch.full_like(qa, 0x7F), torch.full_like(sa, float("nan"))
@@ -600,6 +600,72 @@ def test_captured_graph_follows_new_offsets(fq):
             torch.cuda.synchronize()
             for a, b in zip(out, want[k]):
                 assert same_bits(a, b), k
+    assert fq.device_error() == fq.FP8Q_OK
+
+
+def test_capture_between_copies_and_joined_streams(fq):
+    """Captured calls whose predecessors are copies, fills and events of another stream: the
+    launches that overlap the kernel before them wait for those as well."""
+    M, N, K, E = 400, 256, 384, 3
+    qw, sw, _ = weights(fq, E, N, K, 3145)
+    gamma = workloads.gamma_bf16(K, 0, 3146, DEV)
+    o = dev_offsets(np.array([0, 128, 129, 400], np.int32))
+    x = workloads.activations_bf16((M, K), 0, 3147, DEV)
+    res = workloads.activations_bf16((M, K), 0, 3148, DEV)
+    stage, h = torch.empty_like(x), torch.empty_like(x)
+    q = torch.empty((M, K), dtype=torch.uint8, device=DEV)
+    s = torch.empty((K // 128, M), device=DEV)
+    P = fq.grouped_padded_rows(M, E)
+    t = torch.empty((K, P), dtype=torch.uint8, device=DEV)
+    ts = torch.empty((P // 128, K), device=DEV)
+    g_row, g_s = torch.empty((M, N), dtype=torch.uint8, device=DEV), torch.empty((2, M), device=DEV)
+    c, cs = torch.empty((N, P), dtype=torch.uint8, device=DEV), torch.empty((P // 128, N), device=DEV)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+    dw = torch.empty((E, N, K), dtype=torch.bfloat16, device=DEV)
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        stage.copy_(x)                                            # memcpy -> kernel
+        fq.add_rmsnorm_quant(stage, res, gamma, 1e-5, h, q, s)
+        stage.zero_()                                             # behind its reader
+        other.wait_stream(torch.cuda.current_stream())            # fork
+        y.zero_()
+        fq.grouped_linear_fwd(q, s, qw, sw, o, y)
+        with torch.cuda.stream(other):
+            fq.grouped_transpose_quant_fp8(q, s, o, t, ts)
+        fq.grouped_transpose_quant_bf16(y, o, g_row, g_s, c, cs)
+        torch.cuda.current_stream().wait_stream(other)            # join
+        fq.grouped_linear_wgrad(c, cs, t, ts, o, dw)
+        q.fill_(0x7F)
+        t.fill_(0x7F)
+        c.fill_(0x7F)
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        step()
+    torch.cuda.synchronize()
+    hq, hs = fq.rmsnorm_quant_alloc((x.float() + res.float()).to(torch.bfloat16), gamma, 1e-5)
+    want = [torch.zeros_like(y), torch.zeros_like(dw)]
+    torch.cuda.synchronize()
+    fq.grouped_linear_fwd(hq, hs, qw, sw, o, want[0])
+    torch.cuda.synchronize()
+    _, _, wc, wcs = fq.grouped_transpose_quant_bf16_alloc(want[0], o)
+    wt, wts = fq.grouped_transpose_quant_fp8_alloc(hq, hs, o)
+    torch.cuda.synchronize()
+    fq.grouped_linear_wgrad(wc, wcs, wt, wts, o, want[1])
+    torch.cuda.synchronize()
+    assert same_bits(y, want[0]) and same_bits(dw, want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        step()
+    for _ in range(20):
+        y.fill_(7.5)
+        dw.fill_(7.5)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        assert same_bits(y, want[0]) and same_bits(dw, want[1])
     assert fq.device_error() == fq.FP8Q_OK
 
 
