@@ -130,6 +130,22 @@ constexpr size_t kGroupedSmemBytes = kSmemBytes + group_table_bytes(kMaxExperts)
 static_assert(kGroupedSmemBytes <= 232448 && kSmemUsed % 4 == 0, "shared memory budget of one sm_100 CTA");
 static_assert(kOffOut % 1024 == 0, "TMA store boxes need 1024-byte alignment");
 
+// Division by a number that the host knows: a multiplication and a shift (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994; exact for
+// 0 <= n < 2^31).
+struct Divider {
+  uint32_t mul, shift;
+  Divider() = default;
+  explicit Divider(int32_t d) {
+    shift = 0;
+    while ((uint64_t{1} << shift) < static_cast<uint64_t>(d)) ++shift;
+    mul = static_cast<uint32_t>(((((uint64_t{1} << shift) - d) << 32) / d) + 1);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(mul, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
 struct GemmParams {
   int32_t M, N, K;
   int32_t mblocks, nblocks, kblocks;
@@ -147,6 +163,9 @@ struct GemmParams {
   int32_t limit;             // rows (forward, DGrad) / 128-row groups (WGrad) that exist
   int32_t bx_step, by_step;  // an expert's step in B's tensor map (reduction, rows)
   int64_t sb_se;             // and in the block scales
+  // WGrad's tiles: one expert's, those of `group` column panels, a row of them, a row of
+  // the last panels
+  Divider by_expert, by_span, by_group, by_last;
 };
 
 // Tile order. Within a group of `group` consecutive column panels (row panels with
@@ -205,10 +224,16 @@ __device__ __forceinline__ GroupTile grouped_tile(int t, const GemmParams& p, co
                                                   const int* first) {
   GroupTile g;
   if (kCol) {
-    const int per = p.mblocks * p.nblocks;
-    const int e = t / per;
-    int mb;
-    tile_coords(t - e * per, p, mb, g.nb);
+    // tile_coords by multiplications: with one slice per expert a tile takes about 1.5 us
+    // and every role decodes it first (64 experts of 1024 x 1024, 128 rows each: 39.2 us
+    // with divisions, 37.4 without)
+    const int e = p.by_expert(t);
+    const int w = t - e * p.mblocks * p.nblocks;
+    const int grp = p.by_span(w);
+    const int v = w - grp * p.group * p.mblocks;
+    const int width = min(p.group, p.nblocks - grp * p.group);
+    const int mb = width == p.group ? p.by_group(v) : p.by_last(v);
+    g.nb = grp * p.group + v - mb * width;
     const int g0 = min(first[e], p.limit), g1 = min(first[e + 1], p.limit);
     g.row0 = mb * kPairM;
     g.lo = 0;
@@ -634,6 +659,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             stored = true;
           }
+        } else if constexpr (kGrouped && kColScaleB) {
+          // few slices per expert make this epilogue a large part of a tile's time: the
+          // 16x256b layout (see the promotion) is stmatrix's, a quarter of the instructions
+          // of 4-byte stores (64 experts of 2048 x 2048, 1000 rows: 111 -> 105 us; 8 of
+          // 4096 x 2048, 1500 rows: 48.7 -> 46.0); dW leaves L2 before the operands do (32
+          // of 2048 x 1024, 768 rows, back to back: 31.6 -> 27.6)
+          if (stored) {  // the previous tile's stores must have read the boxes
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+          }
+          const uint32_t st = smem_u32(out0) + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int hi = 0; hi < 2; ++hi)
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) {
+                  const float* a = acc + ((2 * b + cc) * 8 + k) * 4 + 2 * hi;
+                  stmatrix_x4((st ^ (k << 4)) + cc * kStageOutBytes + (16 * b + 8 * hi) * 128,
+                              pack_bf16x2(a[0], a[1]), pack_bf16x2(a[4], a[5]),
+                              pack_bf16x2(a[8], a[9]), pack_bf16x2(a[12], a[13]));
+                }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const uint64_t policy = policy_evict_first();
+            tma_store_2d(&tmY, out0, col_lo, out_row, policy);
+            if (hi_ok) tma_store_2d(&tmY, out1, col_hi, out_row, policy);
+            tma_store_commit();
+          }
+          stored = true;
         } else {
           if (stored) {  // the previous tile's stores must have read the boxes
             if (lane == 0) tma_store_wait_read();
@@ -872,6 +930,13 @@ fp8q_status launch_grouped(const GroupedGemm& g, cudaStream_t stream) {
   p.limit = static_cast<int32_t>(kCol ? slices : g.rows);
   p.bx_step = static_cast<int32_t>(g.bx_step);
   p.by_step = static_cast<int32_t>(g.by_step);
+  if (kCol) {
+    const int32_t last = p.nblocks % p.group;
+    p.by_expert = Divider(p.mblocks * p.nblocks);
+    p.by_span = Divider(p.group * p.mblocks);
+    p.by_group = Divider(p.group);
+    p.by_last = Divider(last ? last : p.group);
+  }
   p.err = device_error_word();
   p.wait_limit_ns = kWaitLimitNs;
   if (!p.err) return FP8Q_ERR_CUDA;

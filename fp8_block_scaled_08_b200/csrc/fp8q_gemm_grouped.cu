@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmSA);
   }
+  // a successor that allocates TMEM too cannot become resident here before this CTA has
+  // its own: the rings of two grouped product kernels do not fit one SM's shared memory
   let_next_kernel_start();
   if (warp == 1) tmem_alloc<S::kTmemCols>(tmem_slot);
   wait_for_previous_kernel();
