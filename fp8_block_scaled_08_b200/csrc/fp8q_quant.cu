@@ -2869,21 +2869,22 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
 // experts' groups (they restart at each expert; rows past a group's end count as zeros).
 //   A group of four warps owns two stages of the ring (a 128x128 code tile, 128-byte
 //   swizzle, and its row scales) and takes every kRqGroups-th tile of the CTA; a warp takes
-//   32 columns over all 128 rows, so a column's maximum needs only shuffles: lane 8g + c
-//   holds columns 4c .. 4c + 3 (one word a row) of rows 8j + 2g and 8j + 2g + 1 (j < 16);
-//   with the swizzle the four g read four different pairs of 16-byte chunks, free of bank
-//   conflicts. The 32 words stay in registers; the products s * dec(q) are formed twice
-//   (for the maximum and for the codes), since 128 of them would not fit. Codes of 8 rows x 4 columns move between the four g by a 4x4 transpose of
-//   halfwords (two shuffles), after which lane 8g + c holds column 4c + g in row order; it
-//   stages it for the warp's tensor store of 32 columns x 128 codes (stored from registers,
-//   every lane its own 128-byte line, the stores took about 15 us of the memory pipe).
+//   32 columns over all 128 rows, so a column's maximum needs only shuffles: lane 4r + c
+//   holds columns 4c .. 4c + 3 and 16 + 4c .. (two words a row) of rows 16j + r and
+//   16j + r + 8 (j < 8); with the swizzle its reads are free of bank conflicts. The 32 words
+//   stay in registers; the products s * dec(q) are formed twice (for the maximum and for the
+//   codes), since 128 of them would not fit. The layout is that of a transposing stmatrix,
+//   which puts the codes of 16 rows x 32 columns into the warp's staging tile in one
+//   instruction, for a tensor store of 32 columns x 128 codes (stored from registers, every
+//   lane its own 128-byte line, the stores took about 15 us of the memory pipe). The column
+//   maxima meet by halving (seven shuffles), so that every lane forms one column's scale;
+//   the warp reads them back from shared memory.
 //   The last warp is the producer. A group may start at any row, so its row scales come as
 //   a copy of 132 from the multiple of 4 before it.
-// Latency bounds the dense kernel (two CTA barriers a tile, 14.6 warps an SM, 0.32 of the
-// issue slots at 8192 x 4096): its layout took 54.9 us here at 16384 x 4096, this one
-// 42.7 us (3.3 TB/s), 17.7 of them the reads alone; now the instructions bound it (12 per
-// element, 0.6 of the issue slots). Rolled-up loops that read the words twice took 50 us,
-// four or six groups of warps 43-50 us.
+// At 16384 x 4096 over 8 experts: 35.7 us (3.9 TB/s); transposed by two shuffles and seven
+// byte permutations per 8 x 4 codes, every lane forming four scales, 44.9; the dense kernel's
+// layout (two CTA barriers a tile, 14.6 warps an SM) 54.9; the reads alone take 17.7.
+// 301 x 3584 over 16: 6.5 us (8.0). The instructions bound it.
 constexpr int kRqGroups = 3;  // consumer groups of four warps
 constexpr int kRqStages = 2 * kRqGroups;
 constexpr int kRqThreads = 32 * (4 * kRqGroups + 1);
@@ -2893,7 +2894,8 @@ constexpr uint32_t kRqOut = 32 * 128;  // a warp's transposed codes
 constexpr uint32_t kRqOffOut = kRqStages * kRqTile;
 constexpr uint32_t kRqOffScales = kRqOffOut + 4 * kRqGroups * kRqOut;
 constexpr uint32_t kRqOffRows = kRqOffScales + kRqStages * kRqScales;  // int2 per stage
-constexpr uint32_t kRqOffBar = kRqOffRows + kRqStages * 8;
+constexpr uint32_t kRqOffCols = kRqOffRows + kRqStages * 8;  // per warp: 32 scales, reciprocals
+constexpr uint32_t kRqOffBar = kRqOffCols + 4 * kRqGroups * 256;
 constexpr uint32_t kRqOffTab = kRqOffBar + 2 * kRqStages * 8 + 16;
 constexpr size_t requant_smem(int E) { return 1024 + kRqOffTab + group_table_bytes(E); }
 static_assert(requant_smem(kMaxExperts) <= 232448, "shared memory budget of one sm_100 CTA");
@@ -2912,20 +2914,36 @@ __device__ __forceinline__ void dequant4(uint32_t w, float s, float (&x)[4]) {
   mul2(x[2], x[3], b.x, b.y, s, s);
 }
 
-// Four codes of a word: requantized with the columns' scales (none of them tiny). The
-// quotient is quot's with the residual the other way round (x - q s, no negations), which
-// turns -0 into +0; the scales are positive, so a code's sign is that of the code it came
-// from.
-__device__ __forceinline__ uint32_t requant4(uint32_t w, float s, const GroupScale (&g)[4]) {
-  float x[4], t[4];
-  dequant4(w, s, x);
+// Two rows of codes of four columns (wa, wb: a word each), requantized with the columns'
+// scales (none of them tiny): o[p] becomes columns 2p and 2p + 1, row a in the low half.
+// na, nb are the rows' scales with their signs turned, nrs the columns' reciprocals
+// likewise: the quotient is quot's on -x, (t s - x) (-1/s) + t, which keeps the sign of a
+// zero.
+__device__ __forceinline__ void requant_pair(uint32_t wa, uint32_t wb, float na, float nb,
+                                             const float* nrs, const float* s, uint32_t (&o)[2]) {
+  float x[2][4], t[2][4];
+  dequant4(wa, na, x[0]);
+  dequant4(wb, nb, x[1]);
 #pragma unroll
-  for (int c = 0; c < 4; c += 2) {
-    mul2(t[c], t[c + 1], x[c], x[c + 1], g[c].rs, g[c + 1].rs);
-    fma2(x[c], x[c + 1], t[c], t[c + 1], g[c].ns, g[c + 1].ns);
-    fma2(t[c], t[c + 1], x[c], x[c + 1], g[c].rs, g[c + 1].rs);
-  }
-  return cvt_e4m3x4(t[0], t[1], t[2], t[3]) | (w & 0x80808080u);
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+      mul2(t[r][c], t[r][c + 1], x[r][c], x[r][c + 1], nrs[c], nrs[c + 1]);
+      fma2(x[r][c], x[r][c + 1], t[r][c], t[r][c + 1], s[c], s[c + 1]);
+      fma2(t[r][c], t[r][c + 1], x[r][c], x[r][c + 1], nrs[c], nrs[c + 1]);
+    }
+  o[0] = cvt_e4m3x4(t[0][0], t[0][1], t[1][0], t[1][1]);
+  o[1] = cvt_e4m3x4(t[0][2], t[0][3], t[1][2], t[1][3]);
+}
+
+// Four 16x8 blocks of codes to shared memory, transposed (a block's column becomes 16
+// bytes): lane l holds columns 2 (l % 4) and 2 (l % 4) + 1 of rows l / 4 (low half) and
+// l / 4 + 8 of each and gives the address of column l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_t_x4(uint32_t addr, uint32_t b0, uint32_t b1, uint32_t b2,
+                                              uint32_t b3) {
+  asm volatile("stmatrix.sync.aligned.m16n8.x4.trans.shared.b8 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(b0), "r"(b1), "r"(b2), "r"(b3)
+               : "memory");
 }
 
 // 8 rows x 32 columns of codes: ca and cb hold columns 4c .. 4c + 3 of the two rows of
@@ -2963,24 +2981,36 @@ struct RowsToColumns {
 };
 
 // A warp's tile by IEEE division, for a warp that holds a column with a tiny scale: kept
-// out of line and rolled up, away from the registers of the usual path.
-__device__ __noinline__ void requant_tile_div(const uint8_t* worda, const uint8_t* wordb,
-                                              const float* rsc, float4 gs, int rows, int gr,
-                                              uint8_t* orow, int col) {
-  const RowsToColumns<false> to_columns(gr);
+// out of line and rolled up, away from the registers of the usual path. The lanes' rows and
+// columns are those of grouped_requant_kernel; s holds this lane's eight columns' scales.
+__device__ __noinline__ void requant_tile_div(const uint8_t* word0, const uint8_t* word1,
+                                              const float* rsc, const float* cs, int rows, int r0,
+                                              uint32_t line, int swz) {
 #pragma unroll 1
-  for (int j = 0; j < 16; ++j) {
-    uint32_t c[2], o[2];
+  for (int j = 0; j < 8; ++j) {
+    uint32_t o[4];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* word = (h ? word1 : word0) + j * 2048;
+      float x[2][4], t[2][4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      float x[4];
-      dequant4(*reinterpret_cast<const uint32_t*>((b ? wordb : worda) + j * 1024), rsc[8 * j + b], x);
-      c[b] = cvt_e4m3x4(__fdiv_rn(x[0], gs.x), __fdiv_rn(x[1], gs.y), __fdiv_rn(x[2], gs.z),
-                        __fdiv_rn(x[3], gs.w));
-      if (8 * j + 2 * gr + b >= rows) c[b] = 0u;
+      for (int r = 0; r < 2; ++r) {
+        dequant4(*reinterpret_cast<const uint32_t*>(word + r * 1024), rsc[16 * j + 8 * r], x[r]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          t[r][c] = 16 * j + 8 * r + r0 < rows ? __fdiv_rn(x[r][c], cs[16 * h + c]) : 0.0f;
+      }
+      const uint32_t a = cvt_e4m3x4(t[0][0], t[0][1], t[1][0], t[1][1]);
+      const uint32_t b = cvt_e4m3x4(t[0][2], t[0][3], t[1][2], t[1][3]);
+      if (h == 0) {
+        o[0] = a;
+        o[1] = b;
+      } else {
+        o[2] = a;
+        o[3] = b;
+      }
     }
-    to_columns(c[0], c[1], o[0], o[1]);
-    *reinterpret_cast<uint2*>(orow + (((j >> 1) ^ (col & 7)) << 4) + 8 * (j & 1)) = make_uint2(o[0], o[1]);
+    stmatrix_t_x4(line + ((j ^ swz) << 4), o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -3052,16 +3082,15 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
     return;
   }
   // -------------------------------------------------------------- consumers
-  const int grp4 = warp >> 2, gr = lane >> 3, cw = lane & 7;
-  const RowsToColumns<false> to_columns(gr);
-  // this lane's column after the transpose, and its row of the warp's staging tile (128-byte
-  // swizzle: the 16-byte writes of a warp take 4 wavefronts, the least possible)
-  const int col = 4 * cw + gr;
+  const int grp4 = warp >> 2, gr = lane >> 2, cw = lane & 3;
   uint8_t* out = base + kRqOffOut + warp * kRqOut;
-  uint8_t* orow = out + col * 128;
-  const int chunk = 2 * (warp & 3) + (cw >> 2);
-  const uint32_t offa = 2 * gr * 128 + ((chunk ^ (2 * gr)) << 4) + (cw & 3) * 4;
-  const uint32_t offb = (2 * gr + 1) * 128 + ((chunk ^ (2 * gr + 1)) << 4) + (cw & 3) * 4;
+  float* cs = reinterpret_cast<float*>(base + kRqOffCols) + warp * 64;  // scales, -reciprocals
+  // the column whose line this lane addresses in a transposing store, and the column whose
+  // scale it forms
+  const int lcol = 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * ((lane >> 3) & 1) + 16 * (lane >> 4);
+  const int scol = 16 * (lane >> 4) + 4 * cw + 2 * ((lane >> 3) & 1) + ((lane >> 2) & 1);
+  const uint32_t line = smem_u32(out) + lcol * 128;
+  const uint32_t off0 = gr * 128 + (((2 * (warp & 3)) ^ gr) << 4) + cw * 4, off1 = off0 ^ 16;
   int n = 0;
   for (int64_t t = blockIdx.x + static_cast<int64_t>(grp4) * gridDim.x; t < tiles;
        t += static_cast<int64_t>(kRqGroups) * gridDim.x, ++n) {
@@ -3070,69 +3099,91 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
     const int2 rr = stage_rows[b];
     const uint8_t* tile = base + b * kRqTile;
     const float* rsc = reinterpret_cast<const float*>(base + kRqOffScales + b * kRqScales) +
-                       (rr.x & 3) + 2 * gr;
-    uint32_t w[32];
+                       (rr.x & 3) + gr;
+    uint32_t w[8][4];  // [16 rows][columns 0-15: rows gr, gr + 8; columns 16-31: the same]
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      w[2 * j] = *reinterpret_cast<const uint32_t*>(tile + offa + j * 1024);
-      w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(tile + offb + j * 1024);
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        w[j][r] = *reinterpret_cast<const uint32_t*>(tile + off0 + j * 2048 + r * 1024);
+        w[j][2 + r] = *reinterpret_cast<const uint32_t*>(tile + off1 + j * 2048 + r * 1024);
+      }
     }
     if (rr.y < 128) {  // past the group's end: rows of the next expert, or of nobody
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        w[2 * j] = 8 * j + 2 * gr < rr.y ? w[2 * j] : 0u;
-        w[2 * j + 1] = 8 * j + 2 * gr + 1 < rr.y ? w[2 * j + 1] : 0u;
-      }
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (16 * j + 8 * r + gr >= rr.y) w[j][r] = w[j][2 + r] = 0u;
     }
-    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j4 = 0; j4 < 4; ++j4) {
-      if (32 * j4 >= rr.y) break;  // no rows from here on
+    for (int j = 0; j < 8; ++j) {
+      if (16 * j >= rr.y) break;  // no rows from here on
+      const float sa = rsc[16 * j], sb = rsc[16 * j + 8];
 #pragma unroll
-      for (int j = 4 * j4; j < 4 * j4 + 4; ++j) {
+      for (int h = 0; h < 2; ++h) {
         float xa[4], xb[4];
-        dequant4(w[2 * j], rsc[8 * j], xa);
-        dequant4(w[2 * j + 1], rsc[8 * j + 1], xb);
+        dequant4(w[j][2 * h], sa, xa);
+        dequant4(w[j][2 * h + 1], sb, xb);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) m[c] = fmaxf(fmaxf(m[c], fabsf(xa[c])), fabsf(xb[c]));
+        for (int c = 0; c < 4; ++c)
+          m[4 * h + c] = fmaxf(fmaxf(m[4 * h + c], fabsf(xa[c])), fabsf(xb[c]));
       }
     }
-    GroupScale g[4];
+    // the eight lanes of a column meet: each step hands half of the columns over, and lane l
+    // ends with column scol
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      m[c] = fmaxf(m[c], __shfl_xor_sync(kFull, m[c], 8));
-      m[c] = fmaxf(m[c], __shfl_xor_sync(kFull, m[c], 16));
-      g[c] = group_scale_fma(m[c]);
+    for (int d = 4; d >= 1; d >>= 1) {
+      const bool up = lane & (4 * d);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= d) break;
+        const float got = __shfl_xor_sync(kFull, up ? m[c] : m[c + d], 4 * d);
+        m[c] = fmaxf(up ? m[c + d] : m[c], got);
+      }
     }
+    const GroupScale g = group_scale_fma(m[0]);
+    cs[scol] = g.s;
+    cs[32 + scol] = -g.rs;
     const int64_t mb = t / KB, kb = t - mb * KB;
-    const int64_t c0 = kb * 128 + 32 * (warp & 3) + 4 * cw;
-    if (gr == 0 && c0 < K)  // K is a multiple of 16: the four columns are in or out
-      *reinterpret_cast<float4*>(sT + mb * K + c0) = make_float4(g[0].s, g[1].s, g[2].s, g[3].s);
+    const int64_t c0 = kb * 128 + 32 * (warp & 3);
+    if (c0 + scol < K) sT[mb * K + c0 + scol] = g.s;
     if (lane == 0) tma_store_wait_read();  // the previous tile's codes have left
+    const bool small = __any_sync(kFull, g.small);
     __syncwarp();
-    if (__any_sync(kFull, g[0].small || g[1].small || g[2].small || g[3].small)) {
-      requant_tile_div(tile + offa, tile + offb, rsc, make_float4(g[0].s, g[1].s, g[2].s, g[3].s),
-                       rr.y, gr, orow, col);
+    if (small) {
+      requant_tile_div(tile + off0, tile + off1, rsc, cs + 4 * cw, rr.y, gr, line, lcol & 7);
     } else {
+      float s[8], nrs[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<float4*>(s + 4 * h) = *reinterpret_cast<const float4*>(cs + 16 * h + 4 * cw);
+        *reinterpret_cast<float4*>(nrs + 4 * h) =
+            *reinterpret_cast<const float4*>(cs + 32 + 16 * h + 4 * cw);
+      }
       // the products are formed again, not kept: hide that the words are the same
 #pragma unroll
-      for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(w[j]));
+      for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(w[j >> 2][j & 3]));
 #pragma unroll
-      for (int j2 = 0; j2 < 8; ++j2) {
-        uint32_t o[4] = {0u, 0u, 0u, 0u};
+      for (int j = 0; j < 8; ++j) {
+        uint32_t o[2][2] = {{0u, 0u}, {0u, 0u}};
+        if (16 * j < rr.y) {
+          const float na = -rsc[16 * j], nb = -rsc[16 * j + 8];
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          if (32 * (j2 >> 1) >= rr.y) break;  // no rows from here on
-          const int j = 2 * j2 + jj;
-          uint32_t ca = requant4(w[2 * j], rsc[8 * j], g);
-          uint32_t cb = requant4(w[2 * j + 1], rsc[8 * j + 1], g);
+          for (int h = 0; h < 2; ++h)
+            requant_pair(w[j][2 * h], w[j][2 * h + 1], na, nb, nrs + 4 * h, s + 4 * h, o[h]);
           if (rr.y < 128) {  // past the group's end: zero whatever the scale beside it is
-            ca = 8 * j + 2 * gr < rr.y ? ca : 0u;
-            cb = 8 * j + 2 * gr + 1 < rr.y ? cb : 0u;
+            const uint32_t keep = (16 * j + gr < rr.y ? 0xFFFFu : 0u) |
+                                  (16 * j + 8 + gr < rr.y ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              o[h][0] &= keep;
+              o[h][1] &= keep;
+            }
           }
-          to_columns(ca, cb, o[2 * jj], o[2 * jj + 1]);
         }
-        *reinterpret_cast<uint4*>(orow + ((j2 ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        stmatrix_t_x4(line + ((j ^ (lcol & 7)) << 4), o[0][0], o[0][1], o[1][0], o[1][1]);
       }
     }
     fence_proxy_async_smem();
