@@ -2900,12 +2900,6 @@ constexpr uint32_t kRqOffTab = kRqOffBar + 2 * kRqStages * 8 + 16;
 constexpr size_t requant_smem(int E) { return 1024 + kRqOffTab + group_table_bytes(E); }
 static_assert(requant_smem(kMaxExperts) <= 232448, "shared memory budget of one sm_100 CTA");
 
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
-
 // The four products s * dec(q) of a word of codes, each rounded to fp32.
 __device__ __forceinline__ void dequant4(uint32_t w, float s, float (&x)[4]) {
   const float2 a = e4m3x2_to_f32(static_cast<uint16_t>(w));
@@ -2945,40 +2939,6 @@ __device__ __forceinline__ void stmatrix_t_x4(uint32_t addr, uint32_t b0, uint32
                "r"(b0), "r"(b1), "r"(b2), "r"(b3)
                : "memory");
 }
-
-// 8 rows x 32 columns of codes: ca and cb hold columns 4c .. 4c + 3 of the two rows of
-// row pair p(g) (lane 8g + c); o0 and o1 become rows 0-3 and 4-7 of column 4c + g. The row
-// pairs are p(g) = g (rows 2g, 2g + 1) or, kCrossed, 0, 2, 1, 3 for g = 0 .. 3.
-template <bool kCrossed>
-struct RowsToColumns {
-  uint32_t keep, send, sel0, sel1;
-  bool upper;
-  __device__ __forceinline__ explicit RowsToColumns(int gr) {
-    keep = (gr & 1) ? 0x7632u : 0x5410u;
-    send = keep ^ 0x2222u;
-    upper = gr & 2;
-    // after the two exchanges `mine` holds the pairs of g and g ^ 2, `other` those of g ^ 1
-    // and g ^ 3
-    if (kCrossed) {
-      const uint32_t swap = upper ? 0x2222u : 0u;
-      sel0 = ((gr & 1) ? 0x7654u : 0x3210u) ^ swap;
-      sel1 = ((gr & 1) ? 0x3210u : 0x7654u) ^ swap;
-    } else {
-      sel0 = gr == 0 ? 0x5410u : gr == 1 ? 0x1054u : gr == 2 ? 0x7632u : 0x3276u;
-      sel1 = sel0 ^ 0x2222u;
-    }
-  }
-  __device__ __forceinline__ void operator()(uint32_t ca, uint32_t cb, uint32_t& o0,
-                                             uint32_t& o1) const {
-    const uint32_t lo = byte_perm(ca, cb, 0x5140u), hi = byte_perm(ca, cb, 0x7362u);
-    const uint32_t a = upper ? hi : lo;
-    const uint32_t b = __shfl_xor_sync(kFull, upper ? lo : hi, 16);
-    const uint32_t mine = byte_perm(a, b, keep);
-    const uint32_t other = __shfl_xor_sync(kFull, byte_perm(a, b, send), 8);
-    o0 = byte_perm(mine, other, sel0);
-    o1 = byte_perm(mine, other, sel1);
-  }
-};
 
 // A warp's tile by IEEE division, for a warp that holds a column with a tiny scale: kept
 // out of line and rolled up, away from the registers of the usual path. The lanes' rows and
@@ -3210,14 +3170,14 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
 //          the swizzled staging box are free of bank conflicts.
 //   3, 4   128x1 columns, alternate tiles (a group of four warps owns two stages), each
 //          warp 32 columns over all 128 rows as in grouped_requant_kernel: no barrier
-//          between warps; lane 8g + c holds columns 4c .. 4c + 3 of two rows of every eight,
-//          rows 0, 4, 2, 6 and the next one for g = 0 .. 3 (which with the swizzle puts the
-//          two g of a half-warp's 8-byte reads into different halves of the row).
-// 56.2 us (4.9 TB/s) at 16384 x 4096 over 8 experts, 10.3 us at 301 x 3584 over 16; with
-// quot2's three operations 60.7 and 10.6, in the dense kernel's layout (eight column warps
-// that meet twice a tile) 60.7 and 11.7. Of the 60.7 the tile copies alone took 29.7, with
-// the rows 40.5, with the columns 45.0: both passes are bound by their instructions (about
-// 15 per element in all, now 14), not by the memory.
+//          between warps, the codes transposed by stmatrix, one scale formed per lane (its
+//          8-byte reads of the tile meet in pairs on their banks; no lane layout of stmatrix
+//          avoids that, and the pipe has room).
+// 51.1 us (5.3 TB/s) at 16384 x 4096 over 8 experts, 9.6 us at 301 x 3584 over 16. With the
+// codes transposed by shuffles and every lane forming four scales 56.6 and 10.4; with quot2's
+// three operations as well 60.7 and 10.6; in the dense kernel's layout (eight column warps
+// that meet twice a tile) 60.7 and 11.7. Of the 60.7 the tile copies alone took 29.7: the
+// instructions bound it, not the memory.
 constexpr int kGgStages = 4;
 constexpr int kGgThreads = 640;
 constexpr uint32_t kGgRegsRow = 88, kGgRegsCol = 136, kGgRegsRest = 24;
@@ -3228,7 +3188,8 @@ constexpr uint32_t kGgTile = 2 * kGgBox;
 constexpr uint32_t kGgOffCol = kGgStages * kGgTile;         // 8 x [32 columns][128 codes]
 constexpr uint32_t kGgOffRow = kGgOffCol + 8 * 32 * 128;    // 8 x [16 rows][128 codes]
 constexpr uint32_t kGgOffTab = kGgOffRow + 8 * 16 * 128;    // scale and reciprocal tables
-constexpr uint32_t kGgOffRows = kGgOffTab + 384 * 4;        // int2 per stage
+constexpr uint32_t kGgOffCols = kGgOffTab + 384 * 4;        // 8 x scales, reciprocals (96)
+constexpr uint32_t kGgOffRows = kGgOffCols + 8 * 96 * 4;    // int2 per stage
 constexpr uint32_t kGgOffBar = kGgOffRows + kGgStages * 8;
 constexpr uint32_t kGgOffOffsets = kGgOffBar + 2 * kGgStages * 8 + 16;
 constexpr size_t grouped_grad_smem(int E) { return 1024 + kGgOffOffsets + group_table_bytes(E); }
@@ -3349,36 +3310,45 @@ __device__ __forceinline__ uint2 codes8_recip(const uint4& w, const GroupRecip& 
   return make_uint2(cvt_e4m3x4(t[0], t[1], t[2], t[3]), cvt_e4m3x4(t[4], t[5], t[6], t[7]));
 }
 
-// Four codes of a row: two packed BF16 pairs with the scales of their columns.
-__device__ __forceinline__ uint32_t codes4_cols(uint2 w, const GroupRecip (&g)[4]) {
-  float t[4];
-  quot2_recip(bf16_lo(w.x), bf16_hi(w.x), g[0], g[1], t[0], t[1]);
-  quot2_recip(bf16_lo(w.y), bf16_hi(w.y), g[2], g[3], t[2], t[3]);
-  return cvt_e4m3x4(t[0], t[1], t[2], t[3]);
-}
-__device__ __forceinline__ uint32_t codes4_cols_div(uint2 w, const float (&s)[4]) {
-  return cvt_e4m3x4(__fdiv_rn(bf16_lo(w.x), s[0]), __fdiv_rn(bf16_hi(w.x), s[1]),
-                    __fdiv_rn(bf16_lo(w.y), s[2]), __fdiv_rn(bf16_hi(w.y), s[3]));
+// Two rows of four columns (two packed BF16 pairs each) with the columns' reciprocals:
+// o[p] becomes the codes of columns 2p and 2p + 1, row a in the low half.
+__device__ __forceinline__ void codes_pair(uint2 wa, uint2 wb, const float* hi, const float* lo,
+                                           uint32_t (&o)[2]) {
+  const uint32_t a[2] = {wa.x, wa.y}, b[2] = {wb.x, wb.y};
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float t[4];
+    mul2(t[0], t[1], bf16_lo(a[p]), bf16_hi(a[p]), lo[2 * p], lo[2 * p + 1]);
+    mul2(t[2], t[3], bf16_lo(b[p]), bf16_hi(b[p]), lo[2 * p], lo[2 * p + 1]);
+    fma2(t[0], t[1], bf16_lo(a[p]), bf16_hi(a[p]), hi[2 * p], hi[2 * p + 1]);
+    fma2(t[2], t[3], bf16_lo(b[p]), bf16_hi(b[p]), hi[2 * p], hi[2 * p + 1]);
+    o[p] = cvt_e4m3x4(t[0], t[1], t[2], t[3]);
+  }
 }
 
 // A column warp's tile where some column has to divide: rolled up and out of line, away
-// from the registers of the usual path.
-__device__ __noinline__ void grad_tile_div(const uint8_t* worda, const uint8_t* wordb,
-                                           const float* amax, int rows, int gr, int row0,
-                                           uint8_t* orow, int col) {
-  const RowsToColumns<true> to_columns(gr);
-  float sc[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) sc[c] = group_scale(amax[c]).s;
+// from the registers of the usual path (as requant_tile_div; s holds the columns' scales).
+__device__ __noinline__ void grad_tile_div(const uint8_t* word0, const uint8_t* word1,
+                                           const float* s, int rows, int r0, uint32_t line,
+                                           int swz) {
 #pragma unroll 1
-  for (int j = 0; j < 16; ++j) {
-    uint2 wa = *reinterpret_cast<const uint2*>(worda + j * 1024);
-    uint2 wb = *reinterpret_cast<const uint2*>(wordb + j * 1024);
-    if (8 * j + row0 >= rows) wa = make_uint2(0u, 0u);
-    if (8 * j + row0 + 1 >= rows) wb = make_uint2(0u, 0u);
-    uint32_t o0, o1;
-    to_columns(codes4_cols_div(wa, sc), codes4_cols_div(wb, sc), o0, o1);
-    *reinterpret_cast<uint2*>(orow + (((j >> 1) ^ (col & 7)) << 4) + 8 * (j & 1)) = make_uint2(o0, o1);
+  for (int j = 0; j < 8; ++j) {
+    uint32_t o[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float t[2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint2 w = *reinterpret_cast<const uint2*>((h ? word1 : word0) + j * 2048 + r * 1024);
+        const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          t[r][c] = 16 * j + 8 * r + r0 < rows ? __fdiv_rn(x[c], s[16 * h + c]) : 0.0f;
+      }
+      o[2 * h] = cvt_e4m3x4(t[0][0], t[0][1], t[1][0], t[1][1]);
+      o[2 * h + 1] = cvt_e4m3x4(t[0][2], t[0][3], t[1][2], t[1][3]);
+    }
+    stmatrix_t_x4(line + ((j ^ swz) << 4), o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -3518,16 +3488,17 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
     regs_increase<kGgRegsCol>();
     // ------------------------------------------------------------ 128x1 columns
     const int cg = (warp - 12) >> 2, cw = warp & 3;  // group, 32 columns of the tile
-    const int gr = lane >> 3, c8 = lane & 7;
-    const int x0 = 4 * (gr & 1) + (gr & 2);          // first row of this lane in every eight
-    const int chunk = 4 * (cw & 1) + (c8 >> 1);
-    const uint32_t boff = (cw >> 1) * kGgBox + 8 * (c8 & 1);
-    const uint32_t offa = boff + x0 * 128 + ((chunk ^ x0) << 4);
-    const uint32_t offb = boff + (x0 + 1) * 128 + ((chunk ^ (x0 + 1)) << 4);
-    const RowsToColumns<true> to_columns(gr);
-    const int col = 4 * c8 + gr;  // this lane's column after the transpose
+    const int gr = lane >> 2, c4 = lane & 3;
+    const uint32_t off0 = (cw >> 1) * kGgBox + gr * 128 +
+                          (((4 * (cw & 1) + (c4 >> 1)) ^ gr) << 4) + 8 * (c4 & 1);
+    const uint32_t off1 = off0 ^ 32;  // the columns 16 further on
     uint8_t* out = base + kGgOffCol + (warp - 12) * (32 * 128);
-    uint8_t* orow = out + col * 128;
+    float* cs = reinterpret_cast<float*>(base + kGgOffCols) + (warp - 12) * 96;  // s, hi, lo
+    // the column whose line this lane addresses in a transposing store, and the column whose
+    // scale it forms
+    const int lcol = 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * ((lane >> 3) & 1) + 16 * (lane >> 4);
+    const int scol = 16 * (lane >> 4) + 4 * c4 + 2 * ((lane >> 3) & 1) + ((lane >> 2) & 1);
+    const uint32_t line = smem_u32(out) + lcol * 128;
     int i = cg;
     for (int64_t t = blockIdx.x + static_cast<int64_t>(cg) * gridDim.x; t < tiles;
          t += 2 * static_cast<int64_t>(gridDim.x), i += 2) {
@@ -3535,61 +3506,77 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_grad_kernel(
       if (!mbar_wait_warp(full + b, static_cast<uint32_t>(i / kGgStages) & 1u, ctl)) break;
       const int rows = stage_rows[b].y;
       const uint8_t* tile = base + b * kGgTile;
-      uint2 w[32];
-      uint32_t m0 = 0u, m1 = 0u;
+      uint2 w[8][4];  // [16 rows][columns 0-15: rows gr, gr + 8; columns 16-31: the same]
+      uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        w[2 * j] = *reinterpret_cast<const uint2*>(tile + offa + j * 1024);
-        w[2 * j + 1] = *reinterpret_cast<const uint2*>(tile + offb + j * 1024);
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          w[j][r] = *reinterpret_cast<const uint2*>(tile + off0 + j * 2048 + r * 1024);
+          w[j][2 + r] = *reinterpret_cast<const uint2*>(tile + off1 + j * 2048 + r * 1024);
+        }
       }
       if (rows < 128) {  // past the group's end: rows of the next expert, or of nobody
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (8 * j + x0 >= rows) w[2 * j] = make_uint2(0u, 0u);
-          if (8 * j + x0 + 1 >= rows) w[2 * j + 1] = make_uint2(0u, 0u);
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (16 * j + 8 * r + gr >= rows) w[j][r] = w[j][2 + r] = make_uint2(0u, 0u);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[k & 2] = bf16x2_maxabs_xs(m[k & 2], w[j][k].x);
+          m[(k & 2) + 1] = bf16x2_maxabs_xs(m[(k & 2) + 1], w[j][k].y);
+        }
+      // the eight lanes of a column meet: two steps hand half of the columns over, and lane
+      // l ends with column scol
+#pragma unroll
+      for (int d = 2; d >= 1; d >>= 1) {
+        const bool up = lane & (8 * d);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c >= d) break;
+          const uint32_t got = __shfl_xor_sync(kFull, up ? m[c] : m[c + d], 8 * d);
+          m[c] = bf16x2_maxabs_xs(up ? m[c + d] : m[c], got);
         }
       }
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        m0 = bf16x2_maxabs_xs(m0, w[j].x);
-        m1 = bf16x2_maxabs_xs(m1, w[j].y);
-      }
-#pragma unroll
-      for (int d = 8; d <= 16; d <<= 1) {
-        m0 = bf16x2_maxabs_xs(m0, __shfl_xor_sync(kFull, m0, d));
-        m1 = bf16x2_maxabs_xs(m1, __shfl_xor_sync(kFull, m1, d));
-      }
-      const float amax[4] = {fabsf(bf16_lo(m0)), fabsf(bf16_hi(m0)), fabsf(bf16_lo(m1)),
-                             fabsf(bf16_hi(m1))};
-      GroupRecip g[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) g[c] = group_recip_sm(amax[c], tab);
+      m[0] = bf16x2_maxabs_xs(m[0], __shfl_xor_sync(kFull, m[0], 4));
+      const GroupRecip g = group_recip_sm(fabsf((lane & 4) ? bf16_hi(m[0]) : bf16_lo(m[0])), tab);
+      cs[scol] = g.s;
+      cs[32 + scol] = g.hi;
+      cs[64 + scol] = g.lo;
       const int64_t mb = t / NB, nb = t - mb * NB;
       const int64_t c0 = nb * 128 + 32 * cw;
-      if (gr == 0 && c0 + 4 * c8 < N)  // N is a multiple of 16: the four are in or out
-        *reinterpret_cast<float4*>(s_col + mb * N + c0 + 4 * c8) =
-            make_float4(g[0].s, g[1].s, g[2].s, g[3].s);
+      if (c0 + scol < N) s_col[mb * N + c0 + scol] = g.s;
       if (lane == 0) tma_store_wait_read();  // the previous tile's codes have left
+      const bool small = __any_sync(kFull, g.small);
       __syncwarp();
-      if (__any_sync(kFull, g[0].small || g[1].small || g[2].small || g[3].small)) {
-        grad_tile_div(tile + offa, tile + offb, amax, rows, gr, x0, orow, col);
+      if (small) {
+        grad_tile_div(tile + off0, tile + off1, cs + 4 * c4, rows, gr, line, lcol & 7);
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + b);
       } else {
-        __syncwarp();  // every lane's reads of the tile are complete (their values are used)
+        // every lane's reads of the tile are complete (their values are used)
         if (lane == 0) mbar_arrive(empty + b);
+        float hi[8], lo[8];
 #pragma unroll
-        for (int j2 = 0; j2 < 8; ++j2) {
-          uint32_t o[4] = {0u, 0u, 0u, 0u};
-          if (16 * j2 < rows) {
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<float4*>(hi + 4 * h) =
+              *reinterpret_cast<const float4*>(cs + 32 + 16 * h + 4 * c4);
+          *reinterpret_cast<float4*>(lo + 4 * h) =
+              *reinterpret_cast<const float4*>(cs + 64 + 16 * h + 4 * c4);
+        }
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const int j = 2 * j2 + jj;
-              to_columns(codes4_cols(w[2 * j], g), codes4_cols(w[2 * j + 1], g),
-                         o[2 * jj], o[2 * jj + 1]);
-            }
+        for (int j = 0; j < 8; ++j) {
+          uint32_t o[2][2] = {{0u, 0u}, {0u, 0u}};
+          if (16 * j < rows) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              codes_pair(w[j][2 * h], w[j][2 * h + 1], hi + 4 * h, lo + 4 * h, o[h]);
           }
-          *reinterpret_cast<uint4*>(orow + ((j2 ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          stmatrix_t_x4(line + ((j ^ (lcol & 7)) << 4), o[0][0], o[0][1], o[1][0], o[1][1]);
         }
       }
       fence_proxy_async_smem();
