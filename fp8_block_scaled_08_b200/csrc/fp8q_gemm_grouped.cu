@@ -54,6 +54,7 @@ constexpr int kGmBK = 128;
 constexpr int kGmMaxStages = 8;
 constexpr int kGmScRing = 8;     // row-scale slots (one per stage's slices)
 constexpr uint32_t kGmMaxSmem = 232448;
+constexpr uint32_t kGmStaging = 1024;  // a promotion warp's outputs: 16 tokens x 32 weight rows
 
 template <int kNT>
 struct GmShape {
@@ -68,7 +69,8 @@ struct GmShape {
   static constexpr uint32_t kStage = kWBytes + kXBytes;
   static constexpr uint32_t kSlot = kG * kNT * 4;  // a multiple of 128
   static constexpr uint32_t kBars = 2 * kGmMaxStages + 2 * kBufs + 3 * kGmScRing + 1;
-  static constexpr uint32_t kFixed = kGmScRing * kSlot + kBars * 8 + 16;
+  static constexpr uint32_t kStaging = 4 * kHalves * kGmStaging;
+  static constexpr uint32_t kFixed = kGmScRing * kSlot + kStaging + kBars * 8 + 16;
   static_assert(kBufs % kGmIssuers == 0, "an accumulator buffer is always the same issuer's");
   static_assert(kNT % 32 == 0 && kNT <= 256 && kSlot % 128 == 0, "MMA N and copy alignment");
   static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512,
@@ -123,12 +125,12 @@ __device__ __forceinline__ void gm_wait_drain(uint64_t* bar, uint32_t parity, ui
   }
 }
 
-// 16 or 32 accumulator columns of this warp's lane quarter.
-template <int kC>
-__device__ __forceinline__ void gm_tmem_load(uint32_t taddr, uint32_t (&r)[kC]) {
-  static_assert(kC == 16 || kC == 32, "tcgen05.ld widths");
-  if constexpr (kC == 16) tmem_ld16(taddr, r);
-  else tmem_ld32(taddr, r);
+// 16 lanes x 32 or 64 accumulator columns in the 16x256b shape.
+template <int kR>
+__device__ __forceinline__ void gm_tmem_load(uint32_t taddr, uint32_t (&r)[kR]) {
+  static_assert(kR == 16 || kR == 32, "tcgen05.ld widths");
+  if constexpr (kR == 16) tmem_ld_16x256b_x4(taddr, r);
+  else tmem_ld_16x256b_x8(taddr, r);
 }
 
 template <int kNT>
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int stages = p.stages;
   uint8_t* slots = smem + static_cast<uint32_t>(stages) * S::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(slots + kGmScRing * S::kSlot);
+  uint8_t* staging = slots + kGmScRing * S::kSlot;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + S::kStaging);
   uint64_t* empty = full + kGmMaxStages;
   uint64_t* tfull = empty + kGmMaxStages;
   uint64_t* tempty = tfull + kBufs;
@@ -304,9 +307,17 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const int my_tiles = q < quarters ? num_tiles : 0;  // a low strip leaves quarters idle
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    // columns loaded at a time: 32 per slice, 16 where 64 accumulators leave no room
-    constexpr int kCols = S::kCols, kChunk = kCols == 32 ? 32 : 16;
+    // acc[(2 * b + h) * kCols / 4 + 2 * k + {0, 1}] is weight row 16b + 8h + lane / 4 of the
+    // warp's quarter, tokens 8k + 2 * (lane % 4) + {0, 1} of its warpgroup
+    constexpr int kCols = S::kCols, kOct = kCols / 8;
+    constexpr int kFly = kCols == 32 ? kG : 1;  // slices whose loads are in flight together
     const int col0 = ((warp - kGmPromote) >> 2) * kCols;  // this warpgroup's tokens
+    uint8_t* stg = staging + (warp - kGmPromote) * kGmStaging;
+    // this lane's address in a transposing store of 8 tokens (64-byte lines, the 16-byte
+    // pieces swizzled so that 8 tokens meet all banks), its token and piece in the read back
+    const uint32_t st_put = smem_u32(stg) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    const int tok = lane >> 2, piece = lane & 3;
+    const uint8_t* st_get = stg + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4);
     uint32_t it = 0, si = 0, sph = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < my_tiles; t += gridDim.x) {
@@ -316,29 +327,35 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
       for (int k = 0; k < nst; ++k) {
         const int kb = k * kG;
         if (!mbar_wait_warp(pfull + si, sph, ctl)) { ok = false; break; }
-        const float4* sa = reinterpret_cast<const float4*>(slots + si * S::kSlot) + col0 / 4;
+        const float2* sa = reinterpret_cast<const float2*>(slots + si * S::kSlot) + col0 / 2 + (lane & 3);
         const uint32_t buf = it % kBufs, tph = (it / kBufs) & 1u;
         if (!mbar_wait_warp(tfull + buf, tph, ctl)) { ok = false; break; }
         tc_fence_after();
         const bool whole = kb + kG <= KB;  // a last stage may hold fewer slices
 #pragma unroll
-        for (int c = 0; c < kCols; c += kChunk) {
-          // the loads of all slices of the buffer are in flight together
-          uint32_t r[kG][kChunk];
+        for (int j0 = 0; j0 < kG; j0 += kFly) {
+          uint32_t r[kFly][2][kCols / 2];
 #pragma unroll
-          for (int j = 0; j < kG; ++j)
-            gm_tmem_load<kChunk>(lane_base + (buf * kG + j) * kNT + col0 + c, r[j]);
+          for (int j = 0; j < kFly; ++j)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              gm_tmem_load(lane_base + (static_cast<uint32_t>(16 * b) << 16) + (buf * kG + j0 + j) * kNT + col0,
+                           r[j][b]);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            if (j == 0 || whole) {
+          for (int j = 0; j < kFly; ++j) {
+            if (j0 + j == 0 || whole) {
 #pragma unroll
-              for (int i = 0; i < kChunk; i += 4) {
-                const float4 s4 = sa[(j * kNT + c + i) / 4];  // broadcast
-                float* a = acc + c + i;
-                fma2(a[0], a[1], __uint_as_float(r[j][i]), __uint_as_float(r[j][i + 1]), s4.x, s4.y);
-                fma2(a[2], a[3], __uint_as_float(r[j][i + 2]), __uint_as_float(r[j][i + 3]), s4.z,
-                     s4.w);
+              for (int k = 0; k < kOct; ++k) {
+                const float2 sc = sa[(j0 + j) * (kNT / 2) + 4 * k];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float* a = acc + (2 * b + h) * (kCols / 4) + 2 * k;
+                    const uint32_t* p2 = r[j][b] + 4 * k + 2 * h;
+                    fma2(a[0], a[1], __uint_as_float(p2[0]), __uint_as_float(p2[1]), sc.x, sc.y);
+                  }
               }
             }
           }
@@ -354,17 +371,26 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
       }
       if (!ok) break;
       const GmTile o = gm_tile<kNT>(t, p, off, first);
-      // lanes 2i and 2i + 1 exchange: the even lane stores both outputs of token j, the odd
-      // lane those of token j + 1
-      const int odd = lane & 1;
-      uint16_t* dst = p.y + static_cast<int64_t>(o.row0 + col0 + odd) * p.ldy + o.strip * p.height +
-                      q * 32 + lane - odd;
-      const int lo = o.lo - o.row0 - col0 - odd, hi = o.hi - o.row0 - col0 - odd;
+      uint16_t* dst = p.y + static_cast<int64_t>(o.row0 + col0 + tok) * p.ldy + o.strip * p.height +
+                      q * 32 + 8 * piece;
+      const int lo = o.lo - o.row0 - col0 - tok, hi = o.hi - o.row0 - col0 - tok;
 #pragma unroll
-      for (int j = 0; j < kCols; j += 2) {
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[j] : acc[j + 1], 1);
-        const uint32_t v = odd ? pack_bf16x2(other, acc[j + 1]) : pack_bf16x2(acc[j], other);
-        if (j >= lo && j < hi) *reinterpret_cast<uint32_t*>(dst + j * p.ldy) = v;
+      for (int k = 0; k < kOct; k += 2) {
+#pragma unroll
+        for (int kk = k; kk < k + 2; ++kk) {
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = pack_bf16x2(acc[i * (kCols / 4) + 2 * kk], acc[i * (kCols / 4) + 2 * kk + 1]);
+          stmatrix_trans_x4(st_put + (kk - k) * 512, v[0], v[1], v[2], v[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int kk = k; kk < k + 2; ++kk)
+          if (8 * kk >= lo && 8 * kk < hi)
+            *reinterpret_cast<uint4*>(dst + 8 * kk * p.ldy) =
+                *reinterpret_cast<const uint4*>(st_get + (kk - k) * 512);
+        __syncwarp();
       }
     }
   }
