@@ -23,13 +23,13 @@
 //  * Warp 0 is the producer; warps 1 and 2 issue the MMAs of alternate stages into up to 8
 //    TMEM buffers of kG slices; warp 3 multiplies each slice's token scales by its block
 //    scale, in shared memory; the other warps promote a buffer at a time (figures at
-//    launch_grouped_strips): lane l of warp w holds weight row 32 * (w % 4) + l and the
-//    accumulators of the tile's tokens (of half of them, in two warpgroups, from 64 tokens
-//    on; four warpgroups measured up to 19 % slower) and reads the scale products as
-//    broadcasts (with the products formed by every promoting thread 64- and 128-row tiles
-//    took 2-10 % longer).
-//  * Epilogue: two lanes exchange halves so that each stores two neighbouring outputs of
-//    one token (a warp store writes two runs of 64 bytes).
+//    launch_grouped_strips), in the 16x256b shape: a lane holds 4 weight rows x a quarter of
+//    its warpgroup's tokens (all of them, or half in each of two warpgroups from 64 tokens
+//    on), so that it reads a quarter of the scale products. With a weight row per lane every
+//    lane read all of them, 16-byte broadcasts that filled the shared-memory pipe: 16 experts
+//    of 3584 x 1024, 64 rows each, took 18.7 us, 14.4 this way (four warpgroups: 18.0).
+//  * Epilogue: 16 tokens at a time through shared memory by a transposing stmatrix, so that
+//    a warp stores 64 bytes of each of 8 tokens at once.
 //
 // The first token row of an expert's tiles is rounded down to a multiple of 4 (the row
 // scales come by tensor copy, whose innermost coordinate is a multiple of 16 bytes); rows
@@ -478,19 +478,19 @@ fp8q_status launch_strips(const GroupedGemm& g, int64_t token_tiles, int sms,
 // kernel takes every routing and gives the same bits. Measured, one B200, L2 flushed, us:
 //
 // 1. Where one tile per SM holds the whole product, its time is the serial walk over the
-//    slices: the narrowest tile that fits. One expert of 4096 x 4096, 1 row: 16.4 / 18.5 /
+//    slices: the narrowest tile that fits. One expert of 4096 x 4096, 1 row: 16.4 / 20.5 /
 //    24.6 with tiles of 32 / 64 / 128 token rows, 26.6 with large tiles; 512 x 5120, 300
-//    rows: 18.5 / 18.4 / 24.6, large 30.7; DGrad, 16 experts of 3584 x 1024, at 16 / 32 / 64
-//    rows each: 22.6 / 28.7 / 32.8, 22.5 / 24.6 / 30.7, 24.6 / 26.6 / 26.6, large 28.7 / 30.7 /
-//    30.8. An expert's rows are taken as one and a half times the average (an expert over
-//    the tile's width needs a second tile).
+//    rows: 18.4 / 16.4 / 20.5, large 30.7; DGrad, 16 experts of 3584 x 1024, at 16 / 32 / 64
+//    rows each: 22.6 / 26.7 / 30.7, 22.6 / 22.6 / 28.7, 24.6 / 24.6 / 24.6, large 30.7. An
+//    expert's rows are taken as one and a half times the average (an expert over the tile's
+//    width needs a second tile).
 // 2. Otherwise few rows per expert are bound by the weights (strips), many by the tensor
-//    cores (large tiles). Forward, 64 experts of 4096 x 4096, at 8 / 16 / 32 / 64 / 128 rows
-//    each: 32-row tiles 186 / 186 / 199 / 293 / 510, 64-row 182 / 184 / 193 / 221 / 342, 128-row
-//    238 / 240 / 244 / 248 / 389 (bound by the promotion), large 281 / 289 / 293 / 301 / 309.
-//    Back to back, under the power cap, 2 rows each take 171 with 32-row tiles (6.3 TB/s of
-//    weights, 0.97 of the measured copy rate) and 197 with 64-row tiles.
-//    (Promoting one slice per TMEM buffer instead of two took 198 / 239 at 16 / 32 rows.)
+//    cores (large tiles). Forward, 64 experts of 4096 x 4096, at 16 / 48 / 64 / 96 / 128 / 160
+//    rows each: 32-row tiles 184 / 229 / 274 / 365 / 469 / 565, 64-row 184 / 195 / 209 / 252 /
+//    309 / 354, 128-row 199 / 203 / 205 / 221 / 285 / 328, large 287 / 306 / 310 / 313 / 313 /
+//    333; 8 experts at 192 / 256: 128-row 61 / 72, large 72 / 70. Back to back, under the
+//    power cap, 2 rows each take 159 with 32-row tiles, 162 with 64-row tiles (6.6 TB/s of
+//    weights), 16 rows 168 / 175.
 fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_t stream) {
   taken = true;
   const int sms = sm100_sm_count();
@@ -504,7 +504,8 @@ fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_
   if (token_tiles(64) * strips <= sms) return launch_strips<64>(g, token_tiles(64), sms, stream);
   if (token_tiles(128) * strips <= sms) return launch_strips<128>(g, token_tiles(128), sms, stream);
   if (g.rows <= 16 * g.E) return launch_strips<32>(g, token_tiles(32), sms, stream);
-  if (g.rows <= 96 * g.E) return launch_strips<64>(g, token_tiles(64), sms, stream);
+  if (g.rows <= 56 * g.E) return launch_strips<64>(g, token_tiles(64), sms, stream);
+  if (g.rows <= 192 * g.E) return launch_strips<128>(g, token_tiles(128), sms, stream);
   taken = false;
   return FP8Q_OK;
 }

@@ -170,6 +170,17 @@ def test_products_over_strip_shapes(fq, counts, N, K):
                                                           sw[e].clone())), e
 
 
+@pytest.mark.parametrize("avg", [12, 40, 57, 100, 190, 230])
+@pytest.mark.parametrize("N,K", [(1280, 640), (896, 1408)])
+def test_products_over_many_tiles(fq, avg, N, K):
+    """More tiles than SMs at every choice of kernel: 40 ragged experts, one of them without
+    rows and one with a single row."""
+    rng = np.random.RandomState(avg)
+    counts = [int(c) for c in rng.randint(0, 2 * avg, 40)]
+    counts[7], counts[23] = 0, 1
+    test_products_over_strip_shapes(fq, counts, N, K)
+
+
 def test_strided_outputs_and_wide_scales(fq):
     """Row strides of y and dx, and scale arrays longer than the rows."""
     off, M, E = route("ragged")
