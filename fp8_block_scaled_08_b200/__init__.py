@@ -555,10 +555,8 @@ def linear_wgrad_acc_f32(qdyT, sdy_c, qxT, sx_c, dw, stream=None):
 # --------------------------------------------------------------------------
 
 def _row_stride(t, rows, cols, name):
-    """Row stride of a [rows, cols] matrix with dense rows (a single row has none: its
-    length)."""
-    if t.is_contiguous():
-        return cols
+    """Row stride of a matrix [rows, cols] that is not contiguous, with dense rows (a single
+    row has none: its length)."""
     r, c = t.stride()
     if c != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
@@ -588,7 +586,8 @@ def _run(fn, where, stream, dev, *args):
 
 
 def _device(names, *operands):
-    """The CUDA device on which all operands (None: not given) lie."""
+    """Refuse operands (None: not given) that do not lie on one CUDA device, by name; the
+    callers compare the devices themselves first."""
     dev = operands[0].get_device()
     if dev < 0:
         raise ValueError("libfp8q takes CUDA tensors (device pointers)")
@@ -596,7 +595,6 @@ def _device(names, *operands):
         if t is not None and t.get_device() != dev:
             name = [n for n, o in zip(names.split(), operands) if o is t][0]
             raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
-    return dev
 
 
 _T, _BF16, _U8, _F32 = torch.Tensor, torch.bfloat16, torch.uint8, torch.float32
@@ -664,10 +662,15 @@ def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
         _exact_dense(gamma, (H,), _BF16, "gamma")
         _exact_dense(q, shape, _U8, "q")
     lds = _scales_dense(s, _groups(H), M, "s")
-    dev = _device("x res gamma h q s", x, res, gamma, h, q, s)
+    dev = x.get_device()
+    if not (0 <= dev == res.get_device() == gamma.get_device() == h.get_device()
+            == q.get_device() == s.get_device()):
+        _device("x res gamma h q s", x, res, gamma, h, q, s)
     _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, dev, x.data_ptr(),
-         res.data_ptr(), gamma.data_ptr(), M, H, _row_stride(x, M, H, "x"),
-         _row_stride(res, M, H, "res"), float(eps), h.data_ptr(), _row_stride(h, M, H, "h"),
+         res.data_ptr(), gamma.data_ptr(), M, H,
+         H if x.is_contiguous() else _row_stride(x, M, H, "x"),
+         H if res.is_contiguous() else _row_stride(res, M, H, "res"), float(eps), h.data_ptr(),
+         H if h.is_contiguous() else _row_stride(h, M, H, "h"),
          q.data_ptr(), s.data_ptr(), lds)
 
 
@@ -725,10 +728,13 @@ def grouped_linear_fwd(qa, sa, qw, sw, offsets, y, stream=None):
     E, N, K = _grouped_weight(qw, sw, offsets, "qw", 1)
     M, lds = _grouped_rows(qa, sa, K, "qa", "sa")
     _exact(y, (M, N), torch.bfloat16, "y")
-    dev = _device("qa sa qw sw offsets y", qa, sa, qw, sw, offsets, y)
+    dev = qa.get_device()
+    if not (0 <= dev == sa.get_device() == qw.get_device() == sw.get_device()
+            == offsets.get_device() == y.get_device()):
+        _device("qa sa qw sw offsets y", qa, sa, qw, sw, offsets, y)
     _run(_lib.fp8q_grouped_linear_fwd, "fp8q_grouped_linear_fwd", stream, dev, qa.data_ptr(),
          sa.data_ptr(), lds, qw.data_ptr(), sw.data_ptr(), offsets.data_ptr(), E, M, N, K,
-         y.data_ptr(), _row_stride(y, M, N, "y"))
+         y.data_ptr(), N if y.is_contiguous() else _row_stride(y, M, N, "y"))
 
 
 def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
@@ -737,10 +743,13 @@ def grouped_linear_dgrad(qdy, sdy, qwT, sw, offsets, dx, stream=None):
     E, N, K = _grouped_weight(qwT, sw, offsets, "qwT", 2)
     M, lds = _grouped_rows(qdy, sdy, N, "qdy", "sdy")
     _exact(dx, (M, K), torch.bfloat16, "dx")
-    dev = _device("qdy sdy qwT sw offsets dx", qdy, sdy, qwT, sw, offsets, dx)
+    dev = qdy.get_device()
+    if not (0 <= dev == sdy.get_device() == qwT.get_device() == sw.get_device()
+            == offsets.get_device() == dx.get_device()):
+        _device("qdy sdy qwT sw offsets dx", qdy, sdy, qwT, sw, offsets, dx)
     _run(_lib.fp8q_grouped_linear_dgrad, "fp8q_grouped_linear_dgrad", stream, dev, qdy.data_ptr(),
          sdy.data_ptr(), lds, qwT.data_ptr(), sw.data_ptr(), offsets.data_ptr(), E, M, N, K,
-         dx.data_ptr(), _row_stride(dx, M, K, "dx"))
+         dx.data_ptr(), K if dx.is_contiguous() else _row_stride(dx, M, K, "dx"))
 
 
 def _grouped_columns(qT, sT, rows, name_q, name_s):
@@ -770,9 +779,13 @@ def grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, strea
         _exact_dense(q_row, shape, _U8, "q_row")
         lds_row = _scales_dense(s_row, _groups(N), M, "s_row")
     P = _grouped_columns(q_colT, s_col, N, "q_colT", "s_col")
-    dev = _device("dy offsets q_colT s_col q_row s_row", dy, offsets, q_colT, s_col, q_row, s_row)
+    dev = dy.get_device()
+    if not (0 <= dev == offsets.get_device() == q_colT.get_device() == s_col.get_device()
+            and (q_row is None or dev == q_row.get_device() == s_row.get_device())):
+        _device("dy offsets q_colT s_col q_row s_row", dy, offsets, q_colT, s_col, q_row, s_row)
     _run(_lib.fp8q_grouped_transpose_quant_bf16, "fp8q_grouped_transpose_quant_bf16", stream, dev,
-         dy.data_ptr(), offsets.data_ptr(), E, M, N, _row_stride(dy, M, N, "dy"),
+         dy.data_ptr(), offsets.data_ptr(), E, M, N,
+         N if dy.is_contiguous() else _row_stride(dy, M, N, "dy"),
          None if q_row is None else q_row.data_ptr(), None if s_row is None else s_row.data_ptr(),
          lds_row, q_colT.data_ptr(), s_col.data_ptr(), P)
 
@@ -798,7 +811,10 @@ def grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream=None):
     K = q.shape[1]
     M, lds = _grouped_rows(q, s, K, "q", "s")
     P = _grouped_columns(qT, sT, K, "qT", "sT")
-    dev = _device("q s offsets qT sT", q, s, offsets, qT, sT)
+    dev = q.get_device()
+    if not (0 <= dev == s.get_device() == offsets.get_device() == qT.get_device()
+            == sT.get_device()):
+        _device("q s offsets qT sT", q, s, offsets, qT, sT)
     _run(_lib.fp8q_grouped_transpose_quant_fp8, "fp8q_grouped_transpose_quant_fp8", stream, dev,
          q.data_ptr(), s.data_ptr(), offsets.data_ptr(), E, M, K, lds, qT.data_ptr(),
          sT.data_ptr(), P)
@@ -830,7 +846,10 @@ def grouped_linear_wgrad(qdyT, sdy_c, qxT, sx_c, offsets, dw, stream=None):
     if dw.shape[0] != E:
         raise ValueError("dw holds %d experts, offsets %d" % (dw.shape[0], E))
     _exact_dense(dw, (E, N, K), torch.bfloat16, "dw")
-    dev = _device("qdyT sdy_c qxT sx_c offsets dw", qdyT, sdy_c, qxT, sx_c, offsets, dw)
+    dev = qdyT.get_device()
+    if not (0 <= dev == sdy_c.get_device() == qxT.get_device() == sx_c.get_device()
+            == offsets.get_device() == dw.get_device()):
+        _device("qdyT sdy_c qxT sx_c offsets dw", qdyT, sdy_c, qxT, sx_c, offsets, dw)
     _run(_lib.fp8q_grouped_linear_wgrad, "fp8q_grouped_linear_wgrad", stream, dev,
          qdyT.data_ptr(), sdy_c.data_ptr(), qxT.data_ptr(), sx_c.data_ptr(), offsets.data_ptr(),
          E, P, N, K, dw.data_ptr(), K)
