@@ -129,6 +129,11 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
 // every thread passes; it lets its successor start its own preparations with
 // let_next_kernel_start (a successor waits in turn for this kernel to be complete, so the
 // order of all memory operations is that of the stream).
+// A kernel that takes tensor memory allocates it between the two: after the wait, so that
+// it never holds columns that the kernel before it still has to allocate, and before the
+// signal, so that no kernel behind it can hold columns that this one waits for (an
+// allocation blocks until the columns are free, and nothing bounds it). This holds whatever
+// kernels are beside it on the stream, another library's among them.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void wait_for_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

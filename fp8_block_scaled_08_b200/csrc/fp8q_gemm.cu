@@ -332,9 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmY);
     if (kColScaleB) prefetch_tensormap(&tmSB);
   }
-  if (warp == 1) tmem_alloc_pair<kTmemCols>(tmem_slot);
   if constexpr (kGrouped) {
-    let_next_kernel_start();
     wait_for_previous_kernel();
     int* off = reinterpret_cast<int*>(smem + kSmemUsed);
     group_table_fill(off, off + p.experts + 1, p.offsets, p.experts,
@@ -346,9 +344,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       atomicOr(p.err, kErrOffsets);
     __syncwarp();
   }
+  if (warp == 1) tmem_alloc_pair<kTmemCols>(tmem_slot);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  if constexpr (kGrouped) let_next_kernel_start();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.err, p.wait_limit_ns};
   int* const goff = reinterpret_cast<int*>(smem + kSmemUsed);

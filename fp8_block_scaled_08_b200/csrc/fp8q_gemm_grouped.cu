@@ -181,15 +181,13 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmSA);
   }
-  // a successor that allocates TMEM too cannot become resident here before this CTA has
-  // its own: the rings of two grouped product kernels do not fit one SM's shared memory
-  let_next_kernel_start();
-  if (warp == 1) tmem_alloc<S::kTmemCols>(tmem_slot);
   wait_for_previous_kernel();
   group_table_fill(off, first, p.offsets, p.experts, p.rows, p.err, gm_token_tiles<kNT>);
+  if (warp == 1) tmem_alloc<S::kTmemCols>(tmem_slot);  // while warp 0 scans the table
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  let_next_kernel_start();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.err, p.wait_limit_ns};
   const int num_tiles = first[p.experts] * p.strips;
