@@ -141,6 +141,19 @@ __device__ __forceinline__ void wait_for_previous_kernel() {
 __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Loads of such a kernel, after the wait: ordinary ones. The read-only path (ld.global.nc)
+// is for memory that nobody writes while the kernel runs, and this kernel may have been
+// resident while the one before it wrote its operands.
+__device__ __forceinline__ int32_t ld_after_wait(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_after_wait(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // ---------------------------------------------------------------------------
 // TMA (tiled tensor loads, no multicast). The shared-memory destination (or source of

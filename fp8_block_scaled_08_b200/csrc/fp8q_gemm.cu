@@ -493,8 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // next 32 are fetched 16 slices ahead (a global load per slice, even prefetched one
       // slice ahead, measured ~10 % slower)
       auto sb_fetch = [&](int kk) -> float {
-        return (!kColScaleB && lo_ok && kk < kblocks) ? __ldg(sbp + static_cast<int64_t>(kk) * p.sb_sr)
-                                                        : 0.0f;
+        if (kColScaleB || !lo_ok || kk >= kblocks) return 0.0f;
+        const float* at = sbp + static_cast<int64_t>(kk) * p.sb_sr;
+        return kGrouped ? ld_after_wait(at) : __ldg(at);
       };
       float sbv = sb_fetch(lane), sbx = 0.0f;
       for (int kb = 0; kb < kblocks; ++kb) {

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(GmShape<kNT>::kThreads, 1) grouped_strip_kerne
       const GmTile g = gm_tile<kNT>(t, p, off, first);
       const float* sbp = p.sb + g.e * p.sb_se + ((g.strip * p.height) >> 7) * p.sb_sj;
       // 32 slices at a time: lane l holds slice 32 * (kb / 32) + l; the next ones 16 ahead
-      auto sb_fetch = [&](int kk) -> float { return kk < KB ? __ldg(sbp + kk * p.sb_sr) : 0.0f; };
+      auto sb_fetch = [&](int kk) -> float { return kk < KB ? ld_after_wait(sbp + kk * p.sb_sr) : 0.0f; };
       float sbv = sb_fetch(lane), sbx = 0.0f;
       for (int kb = 0; kb < KB; kb += kG) {
         if ((kb & 31) == 16) sbx = sb_fetch(kb + 16 + lane);

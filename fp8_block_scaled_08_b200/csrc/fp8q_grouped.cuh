@@ -21,9 +21,9 @@ namespace fp8q {
 // by all threads at once (a latency, not E of them); one warp then does the two scans.
 template <class Count>
 __device__ __forceinline__ void group_table_fill(int* off, int* first,
-                                                 const int32_t* __restrict__ offsets, int E,
+                                                 const int32_t* offsets, int E,
                                                  int limit, unsigned* err, Count count) {
-  for (int i = threadIdx.x; i <= E; i += blockDim.x) off[i] = __ldg(offsets + i);
+  for (int i = threadIdx.x; i <= E; i += blockDim.x) off[i] = ld_after_wait(offsets + i);
   __syncthreads();
   if (threadIdx.x >= 32) return;
   const int lane = static_cast<int>(lane_id());

@@ -896,8 +896,8 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_cta_kernel(
   }
 }
 
-// 16 bytes of an operand that the same call may also write (the residual stream in place):
-// an ordinary load, not the read-only path.
+// 16 bytes of an operand that the same call may also write (the residual stream in place) or
+// that the kernel before it may have written: an ordinary load, not the read-only path.
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -930,7 +930,7 @@ __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
 // which saves a barrier where the few rows leave most SMs idle.
 template <int kThreads, int kChunks, bool kShare, int kMinCtas = 1>
 __global__ void __launch_bounds__(kThreads, kMinCtas) add_rmsnorm_quant_kernel(
-    const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ gamma, int64_t M,
+    const uint16_t* x, const uint16_t* res, const uint16_t* gamma, int64_t M,
     int64_t H, int64_t ldx, int64_t ldr, float eps, uint16_t* h, int64_t ldh,
     uint8_t* __restrict__ q, float* __restrict__ s, int64_t lds) {
   constexpr int kWarps = kThreads / 32;
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) add_rmsnorm_quant_kernel(
 #pragma unroll
   for (int j = 0; j < kChunks; ++j)
     if (tid + j * kThreads < nch)
-      gm[j] = __ldg(reinterpret_cast<const uint4*>(gamma + (tid + j * kThreads) * 8));
+      gm[j] = ld_stream_v4(gamma + (tid + j * kThreads) * 8);
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x, flip ^= 1) {
     uint4 v[kChunks];
 #pragma unroll

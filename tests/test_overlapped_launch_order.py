@@ -45,6 +45,17 @@ def test_one_wait_and_one_signal(body):
     assert body.count(WAIT) == 1 and body.count(SIGNAL) == 1
 
 
+@pytest.mark.parametrize("body", [b for _, b in KERNELS] + [code("fp8q_grouped.cuh")],
+                         ids=[k for k, _ in KERNELS] + ["fp8q_grouped.cuh"])
+def test_no_read_only_loads(body):
+    """ld.global.nc is for memory that nobody writes while the kernel runs; these kernels may
+    be resident while the one before them still writes. (Forms of a kernel that are not
+    launched that way may keep it.)"""
+    assert "ld.global.nc" not in body and "ld_nc" not in body
+    for line in body.splitlines():
+        assert "__ldg" not in line or "kGrouped ? ld_after_wait(" in line, line
+
+
 @pytest.mark.parametrize("body", [b for _, b in KERNELS if "tmem_alloc" in b],
                          ids=[k for k, b in KERNELS if "tmem_alloc" in b])
 def test_tensor_memory_is_allocated_after_the_wait_and_before_the_signal(body):
