@@ -694,7 +694,11 @@ def grouped_quant_weight_alloc(w, want_t=True, stream=None):
     if N % 128 or K % 128:
         raise ValueError("w must be [E, N, K] with N and K multiples of 128, got %s" % (
             tuple(w.shape),))
-    q, s, qT = quant_weight_alloc(w.view(E * N, K), want_t, stream)
+    dev = w.get_device()
+    if dev < 0:
+        raise ValueError("libfp8q takes CUDA tensors (device pointers)")
+    with torch.cuda.device(dev):  # as the grouped calls: on w's device, the current one or not
+        q, s, qT = quant_weight_alloc(w.view(E * N, K), want_t, stream)
     return (q.view(E, N, K), s.view(E, N // 128, K // 128),
             qT.view(K, E, N) if want_t else None)
 
