@@ -303,11 +303,11 @@ def rmsnorm_quant_dual(x, gamma, eps, q_row, s_row, q_colT, s_col, rstd, stream=
 
 def rmsnorm_quant_dual_alloc(x, gamma, eps, stream=None):
     M, H = x.shape
-    q = _empty((M, H), torch.uint8, x.device)
-    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device)
-    qT = _empty((H, M), torch.uint8, x.device)
-    sT = _empty((_groups(M), H), torch.float32, x.device)
-    r = _empty((M,), torch.float32, x.device)
+    q = _empty((M, H), torch.uint8, x.device, stream)
+    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device, stream)
+    qT = _empty((H, M), torch.uint8, x.device, stream)
+    sT = _empty((_groups(M), H), torch.float32, x.device, stream)
+    r = _empty((M,), torch.float32, x.device, stream)
     rmsnorm_quant_dual(x, gamma, eps, q, s, qT, sT, r, stream)
     return q, s, qT, sT, r
 
@@ -333,10 +333,10 @@ def swiglu_quant_dual(gu, q_row, s_row, q_colT, s_col, stream=None):
 def swiglu_quant_dual_alloc(gu, stream=None):
     M, I2 = gu.shape
     I = I2 // 2
-    q = _empty((M, I), torch.uint8, gu.device)
-    s = _empty((_groups(I), lds_for(M)), torch.float32, gu.device)
-    qT = _empty((I, M), torch.uint8, gu.device)
-    sT = _empty((_groups(M), I), torch.float32, gu.device)
+    q = _empty((M, I), torch.uint8, gu.device, stream)
+    s = _empty((_groups(I), lds_for(M)), torch.float32, gu.device, stream)
+    qT = _empty((I, M), torch.uint8, gu.device, stream)
+    sT = _empty((_groups(M), I), torch.float32, gu.device, stream)
     swiglu_quant_dual(gu, q, s, qT, sT, stream)
     return q, s, qT, sT
 
@@ -368,11 +368,11 @@ def swiglu_bwd_quant_dual(gu, dh, q_row, s_row, q_colT, s_col, dgu=None, stream=
 
 def swiglu_bwd_quant_dual_alloc(gu, dh, want_dgu=False, stream=None):
     M, I2 = gu.shape
-    q = _empty((M, I2), torch.uint8, gu.device)
-    s = _empty((_groups(I2), lds_for(M)), torch.float32, gu.device)
-    qT = _empty((I2, M), torch.uint8, gu.device)
-    sT = _empty((_groups(M), I2), torch.float32, gu.device)
-    dgu = _empty((M, I2), torch.bfloat16, gu.device) if want_dgu else None
+    q = _empty((M, I2), torch.uint8, gu.device, stream)
+    s = _empty((_groups(I2), lds_for(M)), torch.float32, gu.device, stream)
+    qT = _empty((I2, M), torch.uint8, gu.device, stream)
+    sT = _empty((_groups(M), I2), torch.float32, gu.device, stream)
+    dgu = _empty((M, I2), torch.bfloat16, gu.device, stream) if want_dgu else None
     swiglu_bwd_quant_dual(gu, dh, q, s, qT, sT, dgu, stream)
     return q, s, qT, sT, dgu
 
@@ -418,14 +418,14 @@ def rmsnorm_bwd_quant_dual(x, gamma, dy, dres, eps, out, q_row, s_row, q_colT, s
 def rmsnorm_bwd_quant_dual_alloc(x, gamma, dy, dres, eps, stream=None):
     M, H = x.shape
     dev = x.device
-    out = _empty((M, H), torch.bfloat16, dev)
-    q = _empty((M, H), torch.uint8, dev)
-    s = _empty((_groups(H), lds_for(M)), torch.float32, dev)
-    qT = _empty((H, M), torch.uint8, dev)
-    sT = _empty((_groups(M), H), torch.float32, dev)
-    dg = _empty((H,), torch.float32, dev)
+    out = _empty((M, H), torch.bfloat16, dev, stream)
+    q = _empty((M, H), torch.uint8, dev, stream)
+    s = _empty((_groups(H), lds_for(M)), torch.float32, dev, stream)
+    qT = _empty((H, M), torch.uint8, dev, stream)
+    sT = _empty((_groups(M), H), torch.float32, dev, stream)
+    dg = _empty((H,), torch.float32, dev, stream)
     nbytes = rmsnorm_bwd_workspace_bytes(M, H)
-    ws = _empty((max(nbytes, 16),), torch.uint8, dev)
+    ws = _empty((max(nbytes, 16),), torch.uint8, dev, stream)
     rmsnorm_bwd_quant_dual(x, gamma, dy, dres, eps, out, q, s, qT, sT, dg, ws, stream)
     return out, q, s, qT, sT, dg
 
@@ -677,9 +677,9 @@ def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
 def add_rmsnorm_quant_alloc(x, res, gamma, eps, stream=None):
     """add_rmsnorm_quant into new tensors: (h, q, s)."""
     M, H = x.shape
-    h = _empty((M, H), torch.bfloat16, x.device)
-    q = _empty((M, H), torch.uint8, x.device)
-    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device)
+    h = _empty((M, H), torch.bfloat16, x.device, stream)
+    q = _empty((M, H), torch.uint8, x.device, stream)
+    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device, stream)
     add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream)
     return h, q, s
 
@@ -799,10 +799,10 @@ def grouped_transpose_quant_bf16_alloc(dy, offsets, want_row=True, stream=None):
     no expert and columns past the last group hold whatever the memory held."""
     M, N = dy.shape
     P = grouped_padded_rows(M, _offsets(offsets))
-    q_row = _empty((M, N), torch.uint8, dy.device) if want_row else None
-    s_row = _empty((_groups(N), lds_for(M)), torch.float32, dy.device) if want_row else None
-    q_colT = _empty((N, P), torch.uint8, dy.device)
-    s_col = _empty((P // 128, N), torch.float32, dy.device)
+    q_row = _empty((M, N), torch.uint8, dy.device, stream) if want_row else None
+    s_row = _empty((_groups(N), lds_for(M)), torch.float32, dy.device, stream) if want_row else None
+    q_colT = _empty((N, P), torch.uint8, dy.device, stream)
+    s_col = _empty((P // 128, N), torch.float32, dy.device, stream)
     grouped_transpose_quant_bf16(dy, offsets, q_row, s_row, q_colT, s_col, stream)
     return q_row, s_row, q_colT, s_col
 
@@ -828,8 +828,8 @@ def grouped_transpose_quant_fp8_alloc(q, s, offsets, stream=None):
     """grouped_transpose_quant_fp8 into new tensors: (qT, sT)."""
     M, K = q.shape
     P = grouped_padded_rows(M, _offsets(offsets))
-    qT = _empty((K, P), torch.uint8, q.device)
-    sT = _empty((P // 128, K), torch.float32, q.device)
+    qT = _empty((K, P), torch.uint8, q.device, stream)
+    sT = _empty((P // 128, K), torch.float32, q.device, stream)
     grouped_transpose_quant_fp8(q, s, offsets, qT, sT, stream)
     return qT, sT
 
@@ -868,74 +868,81 @@ def debug_wait_timeout(limit_ns: int, stream=None) -> int:
 # Allocating helpers (torch allocates; the kernels are the ones above)
 # --------------------------------------------------------------------------
 
-def _empty(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, device, stream=None):
+    """A new tensor for a call on `stream`: its memory is taken from that stream's pool. From
+    the current stream's, the call could write what is still in use there (a block freed
+    before the work on it was done), and a workspace could be given away before the call's
+    kernels have used it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def quant_act_1x128_alloc(x, stream=None):
     M, K = x.shape
-    q = _empty((M, K), torch.uint8, x.device)
-    s = _empty((_groups(K), lds_for(M)), torch.float32, x.device)
+    q = _empty((M, K), torch.uint8, x.device, stream)
+    s = _empty((_groups(K), lds_for(M)), torch.float32, x.device, stream)
     quant_act_1x128(x, q, s, stream)
     return q, s
 
 
 def quant_weight_alloc(w, want_t=True, stream=None):
     N, K = w.shape
-    q = _empty((N, K), torch.uint8, w.device)
-    s = _empty((_groups(N), _groups(K)), torch.float32, w.device)
-    qT = _empty((K, N), torch.uint8, w.device) if want_t else None
+    q = _empty((N, K), torch.uint8, w.device, stream)
+    s = _empty((_groups(N), _groups(K)), torch.float32, w.device, stream)
+    qT = _empty((K, N), torch.uint8, w.device, stream) if want_t else None
     quant_weight_128x128(w, q, s, qT, stream)
     return q, s, qT
 
 
 def rmsnorm_quant_alloc(x, gamma, eps, stream=None):
     M, H = x.shape
-    q = _empty((M, H), torch.uint8, x.device)
-    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device)
+    q = _empty((M, H), torch.uint8, x.device, stream)
+    s = _empty((_groups(H), lds_for(M)), torch.float32, x.device, stream)
     rmsnorm_quant(x, gamma, eps, q, s, stream)
     return q, s
 
 
 def swiglu_quant_alloc(gu, stream=None):
     M, I2 = gu.shape
-    q = _empty((M, I2 // 2), torch.uint8, gu.device)
-    s = _empty((_groups(I2 // 2), lds_for(M)), torch.float32, gu.device)
+    q = _empty((M, I2 // 2), torch.uint8, gu.device, stream)
+    s = _empty((_groups(I2 // 2), lds_for(M)), torch.float32, gu.device, stream)
     swiglu_quant(gu, q, s, stream)
     return q, s
 
 
 def transpose_quant_bf16_alloc(dy, want_row=True, stream=None):
     M, N = dy.shape
-    q_row = _empty((M, N), torch.uint8, dy.device) if want_row else None
-    s_row = _empty((_groups(N), lds_for(M)), torch.float32, dy.device) if want_row else None
-    q_colT = _empty((N, M), torch.uint8, dy.device)
-    s_col = _empty((_groups(M), N), torch.float32, dy.device)
+    q_row = _empty((M, N), torch.uint8, dy.device, stream) if want_row else None
+    s_row = _empty((_groups(N), lds_for(M)), torch.float32, dy.device, stream) if want_row else None
+    q_colT = _empty((N, M), torch.uint8, dy.device, stream)
+    s_col = _empty((_groups(M), N), torch.float32, dy.device, stream)
     transpose_quant_bf16(dy, q_row, s_row, q_colT, s_col, stream)
     return q_row, s_row, q_colT, s_col
 
 
 def transpose_quant_fp8_alloc(q, s, stream=None):
     M, K = q.shape
-    qT = _empty((K, M), torch.uint8, q.device)
-    sT = _empty((_groups(M), K), torch.float32, q.device)
+    qT = _empty((K, M), torch.uint8, q.device, stream)
+    sT = _empty((_groups(M), K), torch.float32, q.device, stream)
     transpose_quant_fp8(q, s, qT, sT, stream)
     return qT, sT
 
 
 def linear_fwd_alloc(qa, sa, qw, sw, stream=None):
-    y = _empty((qa.shape[0], qw.shape[0]), torch.bfloat16, qa.device)
+    y = _empty((qa.shape[0], qw.shape[0]), torch.bfloat16, qa.device, stream)
     linear_fwd(qa, sa, qw, sw, y, stream)
     return y
 
 
 def linear_dgrad_alloc(qdy, sdy, qwT, sw, stream=None):
-    dx = _empty((qdy.shape[0], qwT.shape[0]), torch.bfloat16, qdy.device)
+    dx = _empty((qdy.shape[0], qwT.shape[0]), torch.bfloat16, qdy.device, stream)
     linear_dgrad(qdy, sdy, qwT, sw, dx, stream)
     return dx
 
 
 def linear_wgrad_alloc(qdyT, sdy_c, qxT, sx_c, stream=None):
-    dw = _empty((qdyT.shape[0], qxT.shape[0]), torch.bfloat16, qdyT.device)
+    dw = _empty((qdyT.shape[0], qxT.shape[0]), torch.bfloat16, qdyT.device, stream)
     linear_wgrad(qdyT, sdy_c, qxT, sx_c, dw, stream)
     return dw

@@ -226,3 +226,24 @@ def test_nan_scales_beside_an_expert(fq):  # noqa: F811
             assert torch.equal(sT2[g:g + k], sT[g:g + k]), (e, bad)
         g += k
     assert fq.device_error() == fq.FP8Q_OK
+
+
+def test_outputs_on_another_stream_do_not_meet_a_freed_block(fq):  # noqa: F811
+    """A block that the current stream still writes when it is freed is not what a call on
+    another stream gets for its outputs."""
+    M, H = 256, 1024
+    x = workloads.activations_bf16((M, H), 0, 3350, DEV)
+    res = workloads.activations_bf16((M, H), 0, 3351, DEV)
+    gamma = workloads.gamma_bf16(H, 0, 3352, DEV)
+    want = [t.clone() for t in fq.add_rmsnorm_quant_alloc(x, res, gamma, 1e-5)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.empty_like(t) for t in want]
+    torch.cuda._sleep(20_000_000)  # about 10 ms of the current stream
+    for t in old:
+        t.fill_(1)
+    del old, t
+    got = fq.add_rmsnorm_quant_alloc(x, res, gamma, 1e-5, stream=side)
+    torch.cuda.synchronize()
+    assert same_bits(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[2], want[2])

@@ -45,3 +45,66 @@ def test_weights_are_quantized_on_their_own_device(monkeypatch):
 def test_weights_on_the_host_are_refused():
     with pytest.raises(ValueError, match="CUDA tensors"):
         fq.grouped_quant_weight_alloc(torch.zeros(2, 128, 256, dtype=torch.bfloat16))
+
+
+def bf16(*s):
+    return torch.zeros(s, dtype=torch.bfloat16)
+
+
+def u8(*s):
+    return torch.zeros(s, dtype=torch.uint8)
+
+
+OFF = torch.zeros(3, dtype=torch.int32)
+M, N, K = 128, 128, 256
+ALLOC = {
+    "add_rmsnorm_quant": (bf16(M, N), bf16(M, N), bf16(N), 1e-5),
+    "grouped_transpose_quant_bf16": (bf16(M, N), OFF),
+    "grouped_transpose_quant_fp8": (u8(M, N), torch.zeros(1, M), OFF),
+    "quant_act_1x128": (bf16(M, N),),
+    "quant_weight": (bf16(M, N),),
+    "rmsnorm_quant": (bf16(M, N), bf16(N), 1e-5),
+    "rmsnorm_quant_dual": (bf16(M, N), bf16(N), 1e-5),
+    "rmsnorm_bwd_quant_dual": (bf16(M, N), bf16(N), bf16(M, N), None, 1e-5),
+    "swiglu_quant": (bf16(M, 2 * N),),
+    "swiglu_quant_dual": (bf16(M, 2 * N),),
+    "swiglu_bwd_quant_dual": (bf16(M, 2 * N), bf16(M, N)),
+    "transpose_quant_bf16": (bf16(M, N),),
+    "transpose_quant_fp8": (u8(M, N), torch.zeros(1, M)),
+    "linear_fwd": (u8(M, K), torch.zeros(2, M), u8(N, K), torch.zeros(1, 2)),
+    "linear_dgrad": (u8(M, N), torch.zeros(1, M), u8(K, N), torch.zeros(1, 2)),
+    "linear_wgrad": (u8(N, M), torch.zeros(1, N), u8(K, M), torch.zeros(1, K)),
+}
+
+
+def test_every_allocating_form_is_listed():
+    forms = {n[:-len("_alloc")] for n in dir(fq) if n.endswith("_alloc") and not n.startswith("_")}
+    # the stacked weights are quantize_weight's outputs; split-K allocates in the library
+    assert forms - set(ALLOC) <= {"grouped_quant_weight", "linear_fwd_splitk_no"}
+
+
+class Stream:
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("name", list(ALLOC))
+def test_outputs_belong_to_the_stream_of_the_call(monkeypatch, name):
+    """Outputs (and a workspace) of a call on another stream are allocated in that stream."""
+    log, side = [], Stream()
+    empty = torch.empty
+
+    def alloc(*a, **k):
+        log.append("empty")
+        return empty(*a, **k)
+
+    monkeypatch.setattr(torch.cuda, "stream", recorder(log, "stream"))
+    monkeypatch.setattr(torch, "empty", alloc)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        getattr(fq, name + "_alloc")(*ALLOC[name], stream=side)
+    assert log and len(log) % 3 == 0
+    for i in range(0, len(log), 3):
+        assert log[i:i + 3] == [("stream", side), "empty", ("stream", None)], log
+    log.clear()
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        getattr(fq, name + "_alloc")(*ALLOC[name])
+    assert log and set(log) == {"empty"}
