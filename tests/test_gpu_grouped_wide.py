@@ -247,3 +247,44 @@ def test_outputs_on_another_stream_do_not_meet_a_freed_block(fq):  # noqa: F811
     torch.cuda.synchronize()
     assert same_bits(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(got[2], want[2])
+
+
+def test_weights_past_32_bits(fq):  # noqa: F811
+    """More than 2^31 codes of stacked weights (and elements of dW): the last expert."""
+    E, N, K, n = 132, 4096, 4096, 70
+    w = torch.empty((E, N, K), dtype=torch.bfloat16, device=DEV)
+    for e in range(E):
+        w[e].normal_(std=0.02)
+    qw, sw, qwT = fq.grouped_quant_weight_alloc(w)
+    q1, s1, q1T = fq.quant_weight_alloc(w[-1])
+    assert torch.equal(qw[-1], q1) and torch.equal(sw[-1], s1) and torch.equal(qwT[:, -1], q1T)
+    del w
+    o = torch.tensor([0] * E + [n], dtype=torch.int32, device=DEV)
+    x = workloads.activations_bf16((n, K), 0, 3360, DEV)
+    dy = workloads.gradients_bf16((n, N), 1e-3, 0, 3361, DEV)
+    qa, sa = fq.quant_act_1x128_alloc(x)
+    qr, sr, qc, sc = fq.grouped_transpose_quant_bf16_alloc(dy, o)
+    xT, xs = fq.grouped_transpose_quant_fp8_alloc(qa, sa, o)
+    y = torch.zeros((n, N), dtype=torch.bfloat16, device=DEV)
+    dx = torch.zeros((n, K), dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_fwd(qa, sa, qw, sw, o, y)
+    fq.grouped_linear_dgrad(qr, sr, qwT, sw, o, dx)
+    dw = torch.full((E, N, K), 7.5, dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_wgrad(qc, sc, xT, xs, o, dw)
+    torch.cuda.synchronize()
+    assert fq.device_error() == fq.FP8Q_OK
+    assert same_bits(y, fq.linear_fwd_alloc(qa, sa, q1, s1))
+    assert same_bits(dx, fq.linear_dgrad_alloc(qr, sr, q1T, s1))
+    assert not torch.any(dw[:-1].view(torch.int16))
+    p = slice(0, 128)
+    assert same_bits(dw[-1], fq.linear_wgrad_alloc(qc[:, p].contiguous(), sc[:1].contiguous(),
+                                                   xT[:, p].contiguous(), xs[:1].contiguous()))
+    # many rows of the last expert: the large tiles
+    M = 200 * E
+    o = torch.tensor([0] * E + [M], dtype=torch.int32, device=DEV)
+    q2, s2 = fq.quant_act_1x128_alloc(x.repeat(M // n + 1, 1)[:M].contiguous())
+    y2 = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_fwd(q2, s2, qw, sw, o, y2)
+    torch.cuda.synchronize()
+    assert fq.device_error() == fq.FP8Q_OK
+    assert same_bits(y2[:n], y) and same_bits(y2[M - M % n:], y[:M % n])
