@@ -121,8 +121,12 @@ fp8q_status fp8q_rmsnorm_quant(const uint16_t* x, const uint16_t* gamma, int64_t
 
 /* a3 with the residual addition in front of it (the pre-norm residual stream of a decoder
  * layer; "Implementación", fused RMSNorm kernels):
- *   h = bf16(fl32(x + res)), then the RMSNorm of h and the 1x128 quantization, bit for bit
- *   fp8q_rmsnorm_quant on h.
+ *   h = bf16(fl32(x + res)), then the RMSNorm of h and the 1x128 quantization, with the
+ *   roundings of fp8q_rmsnorm_quant. Both sum the fp64 squares in an order that goes by M
+ *   and H; where the sums are inexact in fp64, r can be one fp32 step off between the two, or
+ *   between two calls of other sizes, in a row whose 1 / sqrt lies within an fp64 rounding of
+ *   the middle between two floats (about 1 row in 10^10 of normal activations with outliers);
+ *   everything behind r is the same bits.
  *   x, res, h [M][H] BF16 (row strides ldx, ldres, ldh), gamma [H] BF16, q [M][H],
  *   s [G(H)][lds]. h may be x or res itself (same address and stride: the residual stream
  *   updated in place); any other overlap of h with an input is refused (FP8Q_ERR_SHAPE).
