@@ -647,8 +647,9 @@ def grouped_padded_rows(M, E) -> int:
 
 def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
     """a3 behind a residual addition: h = bf16(x + res) [M,H] (may be x or res itself), then
-    RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]. Its backward is
-    rmsnorm_bwd_quant_dual on h."""
+    RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]; M >= 1, H % 16 == 0. Its backward is
+    rmsnorm_bwd_quant_dual on h, for H % 128 == 0 and rows rounded up to a multiple of 128
+    (zeros in h, dy and dres behind row M)."""
     _want(x, _BF16, 2, "x")
     M, H = shape = x.shape
     # one comparison of everything on the way of a correct call; the checks one by one (and

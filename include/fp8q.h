@@ -131,8 +131,13 @@ fp8q_status fp8q_rmsnorm_quant(const uint16_t* x, const uint16_t* gamma, int64_t
  *   s [G(H)][lds]. h may be x or res itself (same address and stride: the residual stream
  *   updated in place); any other overlap of h with an input is refused (FP8Q_ERR_SHAPE).
  * The backward is fp8q_rmsnorm_bwd_quant_dual on h with dres = the gradient of h that
- * arrives along the residual stream: its `out` is the gradient of both x and res.
- * Requires H % 16 == 0, H <= 16384. */
+ * arrives along the residual stream: its `out` is the gradient of both x and res. It takes
+ * multiples of 128 only, H % 128 == 0 and M % 128 == 0. For any other M give it buffers with
+ * the rows rounded up to 128 and zeros in h, dy and dres behind row M (eps > 0): `out` is
+ * zero there and they add nothing to dgamma or to a column's group. There is no backward for
+ * another H.
+ * Requires M >= 1 (a call without rows is the caller's to leave out), H % 16 == 0,
+ * H <= 16384. */
 fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t* res,
                                    const uint16_t* gamma, int64_t M, int64_t H, int64_t ldx,
                                    int64_t ldres, float eps, uint16_t* h, int64_t ldh,
