@@ -647,7 +647,7 @@ def grouped_padded_rows(M, E) -> int:
 
 def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
     """a3 behind a residual addition: h = bf16(x + res) [M,H] (may be x or res itself), then
-    RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]; M >= 1, H % 16 == 0. Its backward is
+    RMSNorm(h)*gamma in BF16 -> q [M,H], s [H/128, lds]; H % 16 == 0. Its backward is
     rmsnorm_bwd_quant_dual on h, for H % 128 == 0 and rows rounded up to a multiple of 128
     (zeros in h, dy and dres behind row M)."""
     _want(x, _BF16, 2, "x")
@@ -667,6 +667,8 @@ def add_rmsnorm_quant(x, res, gamma, eps, h, q, s, stream=None):
     if not (0 <= dev == res.get_device() == gamma.get_device() == h.get_device()
             == q.get_device() == s.get_device()):
         _device("x res gamma h q s", x, res, gamma, h, q, s)
+    if M == 0:  # a rank without tokens, as in the grouped calls
+        return
     _run(_lib.fp8q_add_rmsnorm_quant, "fp8q_add_rmsnorm_quant", stream, dev, x.data_ptr(),
          res.data_ptr(), gamma.data_ptr(), M, H,
          H if x.is_contiguous() else _row_stride(x, M, H, "x"),

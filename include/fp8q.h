@@ -136,8 +136,8 @@ fp8q_status fp8q_rmsnorm_quant(const uint16_t* x, const uint16_t* gamma, int64_t
  * the rows rounded up to 128 and zeros in h, dy and dres behind row M (eps > 0): `out` is
  * zero there and they add nothing to dgamma or to a column's group. There is no backward for
  * another H.
- * Requires M >= 1 (a call without rows is the caller's to leave out), H % 16 == 0,
- * H <= 16384. */
+ * Requires M >= 1 (without rows there is nothing to call; the Python binding returns),
+ * H % 16 == 0, H <= 16384. */
 fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x, const uint16_t* res,
                                    const uint16_t* gamma, int64_t M, int64_t H, int64_t ldx,
                                    int64_t ldres, float eps, uint16_t* h, int64_t ldh,

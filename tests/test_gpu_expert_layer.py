@@ -76,3 +76,14 @@ def test_norm_backward_refuses_other_multiples(fq):  # noqa: F811
     for M, H in ((77, 256), (128, 272)):
         with pytest.raises(fq.Fp8qError, match="FP8Q_ERR_SHAPE"):
             fq.rmsnorm_bwd_quant_dual_alloc(e(M, H), e(H), e(M, H), None, EPS)
+
+
+def test_a_rank_without_tokens(fq):  # noqa: F811
+    """No rows: the norm returns, as the grouped calls do, and its checks stay."""
+    e = lambda *n: torch.zeros(n, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    h, q, s = fq.add_rmsnorm_quant_alloc(e(0, 256), e(0, 256), e(256), EPS)
+    assert h.shape == q.shape == (0, 256) and s.shape == (2, 4)
+    with pytest.raises(ValueError, match="gamma"):
+        fq.add_rmsnorm_quant_alloc(e(0, 256), e(0, 256), e(128), EPS)
+    torch.cuda.synchronize()
+    assert fq.device_error() == fq.FP8Q_OK
