@@ -840,7 +840,8 @@ def grouped_transpose_quant_fp8_alloc(q, s, offsets, stream=None):
 def grouped_linear_wgrad(qdyT, sdy_c, qxT, sx_c, offsets, dw, stream=None):
     """linear_wgrad per expert: dw[e] BF16 [N,K] = expert e's groups of qdyT [N,P] x qxT
     [K,P]^T (the outputs of the grouped quantizers, one P for both); zeros for an expert
-    without rows. dw is [E,N,K], dense."""
+    without rows. dw is [E,N,K], dense. Of the offsets only the order and the groups' total
+    against P are checked on the device (the quantizers check them against their rows)."""
     _want(qdyT, torch.uint8, 2, "qdyT"); _want(qxT, torch.uint8, 2, "qxT")
     N, K = qdyT.shape[0], qxT.shape[0]
     if qxT.shape[1] != qdyT.shape[1]:

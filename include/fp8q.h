@@ -349,8 +349,12 @@ fp8q_status fp8q_linear_wgrad_acc_f32(const uint8_t* qdyT, const float* sdy_c,
  * kernels read the offsets, so a call never waits for the host, and a captured graph can
  * be replayed with other offsets. 0 <= offsets[0] <= ... <= offsets[E] <= M: entries that
  * break this are clamped to [0, M] and to the largest entry before them, and reported by
- * fp8q_device_error as FP8Q_ERR_OFFSETS. 1 <= E <= 1024; M = 0 is allowed (nothing to do;
- * pointers that hold no elements may then be NULL).
+ * fp8q_device_error as FP8Q_ERR_OFFSETS (fp8q_grouped_linear_wgrad does not know M and
+ * checks less, see there). 1 <= E <= 1024; M = 0 is allowed (nothing to do, the offsets are
+ * not read; pointers that hold no elements may then be NULL). The kernel of a forward or
+ * DGrad call is chosen by M, E and the widths, since the routing is known on the device only:
+ * every choice gives the same bits, but buffers far larger than the routed rows get the
+ * kernel for many rows.
  *
  * The experts' weights are quantized by one fp8q_quant_weight_128x128 over the stacked
  * [E*N][K] matrix (N % 128 == 0, so no block spans two experts): qw [E][N][K],
@@ -406,8 +410,12 @@ fp8q_status fp8q_grouped_transpose_quant_fp8(const uint8_t* q, const float* s,
  * expert without rows.
  *   qdyT [N][P], sdy_c [P/128][N], qxT [K][P], sx_c [P/128][K] (the same P for both),
  *   dw [E][N][K] BF16 (row stride lddw, experts N * lddw apart).
- * Requires N % 128 == 0, K % 128 == 0, P % 128 == 0, E*N < 2^31. Groups that reach past
- * P are dropped and reported as FP8Q_ERR_OFFSETS. */
+ * Requires N % 128 == 0, K % 128 == 0, P % 128 == 0, E*N < 2^31.
+ * The rows M of the quantizers' call are not an argument: negative and decreasing offsets
+ * are clamped and reported as above, groups that reach past P are dropped and reported, but
+ * offsets beyond M whose groups still fit P are not noticed, and dw then takes in columns
+ * that no quantizer wrote. (The quantizers report such offsets.) With P = 0 the offsets are
+ * not read, every dw[e] is zero and nothing is reported. */
 fp8q_status fp8q_grouped_linear_wgrad(const uint8_t* qdyT, const float* sdy_c,
                                       const uint8_t* qxT, const float* sx_c,
                                       const int32_t* offsets, int64_t E, int64_t P, int64_t N,

@@ -288,3 +288,37 @@ def test_weights_past_32_bits(fq):  # noqa: F811
     torch.cuda.synchronize()
     assert fq.device_error() == fq.FP8Q_OK
     assert same_bits(y2[:n], y) and same_bits(y2[M - M % n:], y[:M % n])
+
+
+def test_wgrad_checks_the_order_and_its_columns(fq):  # noqa: F811
+    """What WGrad notices of wrong offsets, as documented: it does not know the rows, so
+    entries beyond them pass where their groups fit the columns (the quantizers report them);
+    without columns it reads no offsets."""
+    N, K, E, M = 128, 256, 3, 100
+    off = [0, 40, 60, 100]
+    dy = workloads.gradients_bf16((M, N), 1e-3, 0, 3370, DEV)
+    qa, sa = fq.quant_act_1x128_alloc(workloads.activations_bf16((M, K), 0, 3371, DEV))
+    P = fq.grouped_padded_rows(M, E) + 256
+    new = lambda *n, dt=torch.uint8: torch.zeros(n, dtype=dt, device=DEV)  # noqa: E731
+    qdyT, sdy, qxT, sx = new(N, P), new(P // 128, N, dt=torch.float32), new(K, P), new(P // 128, K, dt=torch.float32)
+
+    def wgrad(off):
+        dw = torch.full((E, N, K), 7.5, dtype=torch.bfloat16, device=DEV)
+        fq.grouped_linear_wgrad(qdyT, sdy, qxT, sx, dev_offsets(np.array(off, np.int32)), dw)
+        return dw
+
+    o = dev_offsets(np.array(off, np.int32))
+    fq.grouped_transpose_quant_bf16(dy, o, None, None, qdyT, sdy)
+    fq.grouped_transpose_quant_fp8(qa, sa, o, qxT, sx)
+    want = wgrad(off)
+    assert fq.device_error() == fq.FP8Q_OK
+    beyond = wgrad([0, 40, 60, 300])                        # past M, within P: zero columns here
+    assert fq.device_error() == fq.FP8Q_OK and same_bits(beyond, want)
+    fq.grouped_transpose_quant_fp8(qa, sa, dev_offsets(np.array([0, 40, 60, 300], np.int32)), qxT, sx)
+    assert fq.device_error() == fq.FP8Q_ERR_OFFSETS
+    for bad in ([0, 60, 40, 100], [-1, 40, 60, 100], [0, 40, 60, 60 + P]):
+        wgrad(bad)
+        assert fq.device_error() == fq.FP8Q_ERR_OFFSETS, bad
+    dw = torch.full((E, N, K), 7.5, dtype=torch.bfloat16, device=DEV)
+    fq.grouped_linear_wgrad(qdyT[:, :0], sdy[:0], qxT[:, :0], sx[:0], o, dw)
+    assert fq.device_error() == fq.FP8Q_OK and torch.all(dw == 0)
