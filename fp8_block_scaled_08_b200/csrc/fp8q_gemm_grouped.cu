@@ -17,9 +17,11 @@
 //    expert, the token tiles of a strip next to each other so that they share its weights
 //    in L2); the copies of the next tile start while this one is multiplied, promoted and
 //    stored, so the weight stream does not stop between tiles or experts.
-//  * A ring of stages of kG consecutive slices, up to 200 KB in all: one 3D tensor copy
-//    brings kG * 128 bytes of each of the weight rows, another the token rows of the same
-//    slices (single-slice stages measured 1-4 % slower: twice the copies and barriers).
+//  * A ring of stages of kG consecutive slices, up to 200 KB in all (a strip lower than 128
+//    rows fills a part of each stage: 16 of 40 KB at 32 weight and 32 token rows): one 3D
+//    tensor copy brings kG * 128 bytes of each of the weight rows, another the token rows of
+//    the same slices (single-slice stages measured 1-4 % slower: twice the copies and
+//    barriers).
 //  * Warp 0 is the producer; warps 1 and 2 issue the MMAs of alternate stages into up to 8
 //    TMEM buffers of kG slices; warp 3 multiplies each slice's token scales by its block
 //    scale, in shared memory; the other warps promote a buffer at a time (figures at
@@ -27,7 +29,8 @@
 //    its warpgroup's tokens (all of them, or half in each of two warpgroups from 64 tokens
 //    on), so that it reads a quarter of the scale products. With a weight row per lane every
 //    lane read all of them, 16-byte broadcasts that filled the shared-memory pipe: 16 experts
-//    of 3584 x 1024, 64 rows each, took 18.7 us, 14.4 this way (four warpgroups: 18.0).
+//    of 3584 x 1024, 64 rows each, took 18.7 us, 14.4 this way (four warpgroups: 18.0; captured
+//    calls whose operands stay in L2).
 //  * Epilogue: 16 tokens at a time through shared memory by a transposing stmatrix, so that
 //    a warp stores 64 bytes of each of 8 tokens at once.
 //
@@ -413,8 +416,9 @@ fp8q_status launch_strips(const GroupedGemm& g, int64_t token_tiles, int sms,
   const size_t smem = fixed + static_cast<size_t>(p.stages) * S::kStage;
   // Strip height: 128 rows fill the MMA; where its tiles would leave half of the SMs without
   // one, lower strips (the rest of the MMA's rows is whatever the stage holds, its lanes are
-  // never read) put more SMs on the weights (8 experts of 512 x 2048, 2 rows each: 14.3 us
-  // with 128 rows, 12.4 with 32).
+  // never read) put more SMs on the weights (8 experts of 512 x 2048, 2 rows each, captured
+  // calls: 8.5 to 9.3 us with 128 rows, 8.35 with 32). The stages keep their size, so a lower
+  // strip has less in flight.
   p.height = kGmRows;
   while (p.height > 32 && token_tiles * (g.Ng / p.height) * 2 <= sms) p.height /= 2;
   CUtensorMap tmW, tmX, tmSA;
@@ -472,23 +476,28 @@ fp8q_status launch_strips(const GroupedGemm& g, int64_t token_tiles, int sms,
 
 }  // namespace
 
-// The choice goes by the sizes alone (the routing itself is known on the device only); every
-// kernel takes every routing and gives the same bits. Measured, one B200, L2 flushed, us:
+// The choice goes by the sizes alone (the routing itself is known on the device only: rows
+// is what the buffers hold); every kernel takes every routing and gives the same bits.
+// Measured on one B200, us a call in a captured graph whose calls take other weights each
+// (300 MB or more in all), experts of 0.75 to 1.25 times the average, two runs within 4 %
+// but where a range is given. 64 experts at 16384 rows in buffers of which 128 are routed: 340
+// with the large tiles that rows selects, 159 with buffers of 128 rows.
 //
 // 1. Where one tile per SM holds the whole product, its time is the serial walk over the
-//    slices: the narrowest tile that fits. One expert of 4096 x 4096, 1 row: 16.4 / 20.5 /
-//    24.6 with tiles of 32 / 64 / 128 token rows, 26.6 with large tiles; 512 x 5120, 300
-//    rows: 18.4 / 16.4 / 20.5, large 30.7; DGrad, 16 experts of 3584 x 1024, at 16 / 32 / 64
-//    rows each: 22.6 / 26.7 / 30.7, 22.6 / 22.6 / 28.7, 24.6 / 24.6 / 24.6, large 30.7. An
-//    expert's rows are taken as one and a half times the average (an expert over the tile's
-//    width needs a second tile).
+//    slices: the narrowest tile that fits. One expert of 4096 x 4096, 1 row: 10.5 / 14.4 /
+//    19.3 with tiles of 32 / 64 / 128 token rows, 20.8 with large tiles; 512 x 5120, 300
+//    rows: 12.5 / 12.7 / 15.5, large 25.4; DGrad, 16 experts of 3584 x 1024, at 16 rows each
+//    14.9 / 15.5 / 16.3, large 21.8; at 32, 18.8 / 14.9 / 16.1, large 21.7; at 64, 23.4 /
+//    20.0 / 16.2, large 22.4. An expert's rows are taken as one and a half times the average
+//    (an expert over the tile's width needs a second tile).
 // 2. Otherwise few rows per expert are bound by the weights (strips), many by the tensor
-//    cores (large tiles). Forward, 64 experts of 4096 x 4096, at 16 / 48 / 64 / 96 / 128 / 160
-//    rows each: 32-row tiles 184 / 229 / 274 / 365 / 469 / 565, 64-row 184 / 195 / 209 / 252 /
-//    309 / 354, 128-row 199 / 203 / 205 / 221 / 285 / 328, large 287 / 306 / 310 / 313 / 313 /
-//    333; 8 experts at 192 / 256: 128-row 61 / 72, large 72 / 70. Back to back, under the
-//    power cap, 2 rows each take 159 with 32-row tiles, 162 with 64-row tiles (6.6 TB/s of
-//    weights), 16 rows 168 / 175.
+//    cores (large tiles). Forward, 64 experts of 4096 x 4096, at 16 / 32 / 56 / 80 / 128 /
+//    160 / 192 rows each: 32-row tiles 165 / 198 / 266 / 340 / 482 / 581 / 675, 64-row 168 /
+//    170 / 192-204 / 289 / 375 / 444 / 508, 128-row 225 / 231 / 227 / 259 / 348 / 432 / 444,
+//    large 354 / 358 / 361 / 368 / 361 / 365 / 367; 8 experts at 80 / 128 / 160 / 192: 64-row
+//    38 / 45 / 49 / 60, 128-row 31 / 41-44 / 56 / 55, large 47 / 50 / 51 / 51. Behind a fill
+//    of L2 and a pause of 1 ms, 64 experts at 128 / 160: 128-row 287 / 362, large 310 / 312;
+//    8 experts: 48 / 58, large 52 / 53.
 fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_t stream) {
   taken = true;
   const int sms = sm100_sm_count();
@@ -503,7 +512,7 @@ fp8q_status launch_grouped_strips(const GroupedGemm& g, bool& taken, cudaStream_
   if (token_tiles(128) * strips <= sms) return launch_strips<128>(g, token_tiles(128), sms, stream);
   if (g.rows <= 16 * g.E) return launch_strips<32>(g, token_tiles(32), sms, stream);
   if (g.rows <= 56 * g.E) return launch_strips<64>(g, token_tiles(64), sms, stream);
-  if (g.rows <= 192 * g.E) return launch_strips<128>(g, token_tiles(128), sms, stream);
+  if (g.rows <= 128 * g.E) return launch_strips<128>(g, token_tiles(128), sms, stream);
   taken = false;
   return FP8Q_OK;
 }

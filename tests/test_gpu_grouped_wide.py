@@ -322,3 +322,16 @@ def test_wgrad_checks_the_order_and_its_columns(fq):  # noqa: F811
     dw = torch.full((E, N, K), 7.5, dtype=torch.bfloat16, device=DEV)
     fq.grouped_linear_wgrad(qdyT[:, :0], sdy[:0], qxT[:, :0], sx[:0], o, dw)
     assert fq.device_error() == fq.FP8Q_OK and torch.all(dw == 0)
+
+
+def test_which_kernel_a_call_takes(fq, tmp_path):  # noqa: F811
+    """Strips up to 128 rows per expert, the large tiles above, where one tile per SM does not
+    hold the whole product."""
+    E, N, K = 12, 1152, 256
+    qw, sw, qwT = weights(fq, E, N, K, 3380)
+    new = lambda *n, dt=torch.uint8: torch.zeros(n, dtype=dt, device=DEV)  # noqa: E731
+    for M, kernel in ((1, STRIP), (16 * E + 1, STRIP), (100 * E, STRIP), (128 * E, STRIP),
+                      (128 * E + 1, PAIR), (160 * E, PAIR), (500 * E, PAIR)):
+        o = torch.tensor([i * M // E for i in range(E + 1)], dtype=torch.int32, device=DEV)
+        q, s, y = new(M, K), new(K // 128, fq.lds_for(M), dt=torch.float32), new(M, N, dt=torch.bfloat16)
+        assert kernel_of(lambda: fq.grouped_linear_fwd(q, s, qw, sw, o, y), tmp_path) == kernel, M
