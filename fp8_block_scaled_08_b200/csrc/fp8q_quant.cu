@@ -2881,10 +2881,13 @@ __global__ void __launch_bounds__(256) transpose_quant_fp8_kernel(
 //   the warp reads them back from shared memory.
 //   The last warp is the producer. A group may start at any row, so its row scales come as
 //   a copy of 132 from the multiple of 4 before it.
-// At 16384 x 4096 over 8 experts: 35.7 us (3.9 TB/s); transposed by two shuffles and seven
-// byte permutations per 8 x 4 codes, every lane forming four scales, 44.9; the dense kernel's
-// layout (two CTA barriers a tile, 14.6 warps an SM) 54.9; the reads alone take 17.7.
-// 301 x 3584 over 16: 6.5 us (8.0). The instructions bound it.
+// At 16384 x 4096 over 8 experts, captured calls behind a fill of L2 (its time taken off):
+// 35.7 us (3.9 TB/s); transposed by two shuffles and seven byte permutations per 8 x 4 codes,
+// every lane forming four scales, 44.9; the dense kernel's layout (two CTA barriers a tile,
+// 14.6 warps an SM) 54.9; the reads alone take 17.7. 301 x 3584 over 16: 6.5 us (8.0).
+// Memory does not bound it, and no pipe is full: issue slots 56 %, FMA pipe 43 %, ALU 37 %,
+// shared memory 27 %; a fourth group of warps changed nothing. What does is not established;
+// the stalls are fixed latencies (1.4 of 5.5 cycles an instruction) and busy pipes (0.7).
 constexpr int kRqGroups = 3;  // consumer groups of four warps
 constexpr int kRqStages = 2 * kRqGroups;
 constexpr int kRqThreads = 32 * (4 * kRqGroups + 1);
@@ -3173,11 +3176,13 @@ __global__ void __launch_bounds__(kRqThreads, 1) grouped_requant_kernel(
 //          between warps, the codes transposed by stmatrix, one scale formed per lane (its
 //          8-byte reads of the tile meet in pairs on their banks; no lane layout of stmatrix
 //          avoids that, and the pipe has room).
-// 51.1 us (5.3 TB/s) at 16384 x 4096 over 8 experts, 9.6 us at 301 x 3584 over 16. With the
-// codes transposed by shuffles and every lane forming four scales 56.6 and 10.4; with quot2's
-// three operations as well 60.7 and 10.6; in the dense kernel's layout (eight column warps
-// that meet twice a tile) 60.7 and 11.7. Of the 60.7 the tile copies alone took 29.7: the
-// instructions bound it, not the memory.
+// 51.1 us (5.3 TB/s) at 16384 x 4096 over 8 experts, 9.6 us at 301 x 3584 over 16 (captured
+// calls behind a fill of L2, its time taken off). With the codes transposed by shuffles and
+// every lane forming four scales 56.6 and 10.4; with quot2's three operations as well 60.7
+// and 10.6; in the dense kernel's layout (eight column warps that meet twice a tile) 60.7 and
+// 11.7. Of the 60.7 the tile copies alone took 29.7, so memory does not bound it; nor is a
+// pipe full (issue slots 53 %, ALU 51 %, shared memory 42 %): the warps wait for the tile's
+// words and the barriers (1.8 of 7.8 cycles an instruction) and for fixed latencies (1.6).
 constexpr int kGgStages = 4;
 constexpr int kGgThreads = 640;
 constexpr uint32_t kGgRegsRow = 88, kGgRegsCol = 136, kGgRegsRest = 24;
